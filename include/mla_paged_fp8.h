@@ -318,6 +318,141 @@ mla_status_t mla_merge_lse_parts_bf16(const void* outs, const float* lses, int32
                                       void* out, float* lse, cudaStream_t stream);
 
 /*
+ * Eviction from the latent cache by accumulated attention weight: three entry points that run between
+ * decode steps.  After a decode step, mla_accumulate_weights_fp8 adds to every cached key the softmax
+ * weight it received; when a request has grown past a budget, mla_select_keys names the keys to keep
+ * and mla_compact_paged moves their rows to the front of the request's pages.  The caller then sets
+ * cache_lengths to kept_lengths and frees the pages behind.  With several layers, each layer has its
+ * own weights and its own kept keys, and all have the same kept_lengths, since those depend on the
+ * lengths and the budget alone.  (No counterpart on the reference pages.)
+ *
+ * mla_accumulate_weights_fp8:
+ *     out[b][t] = (t < cache_lengths[b] ? scores[b][t] : 0)
+ *               + sum over query tokens i with t <= cache_lengths[b] + i and heads h of
+ *                 exp(softmax_scale * s_t * <q[b,i,h,:], e4m3(code_t)> - lse[b,i,h])
+ * for t < cache_lengths[b] + max_prompt_length; other entries of out are left as they were.  The
+ * entries of the step's own tokens start at 0.  lse is what the decode of the same step returned.  The
+ * products are those of the unrounded keys e4m3 * s_t (as in mla_decode_paged_fp8_scale_folded, whose
+ * lse makes a row's weights sum to 1 to fp32; with the lse of mla_decode_paged_fp8, which rounds each
+ * key element to bf16, a row's sum is off by that rounding, up to a few 1e-3).  q enters exactly: each
+ * head's row is split into two e4m3 terms after scaling by a power of two (elements below 2^-10 of the
+ * row's largest are off by at most 2^-17 of it).  A (query token, head) whose lse is -inf adds nothing;
+ * a non-finite q row or lse makes the request's sums NaN, a NaN code only its own key's.  Sums are fp32
+ * in a fixed order: results are the same from run to run.
+ *
+ *   q, blocks, ... , shape   as for mla_decode_paged_fp8, with head_dim_granularity 1 (else
+ *                 MLA_ERR_UNSUPPORTED)
+ *   lse           fp32 [batch, max_prompt_length, num_q_heads], natural log, read
+ *   scores        fp32, row b at scores + b * scores_stride; may be NULL (all zero)
+ *   out           fp32, row b at out + b * out_stride; may be scores itself (same stride)
+ * Rows hold at least max_cache_length + max_prompt_length values (else MLA_ERR_INVALID_ARG).  No
+ * workspace: calls on different streams may overlap, and the call can be captured after one call on
+ * the device.  The keys of a page id past the pool are left as they were and flagged
+ * (MLA_ERR_DEVICE_BOUNDS), and a length above max_cache_length is clamped to it and flagged.
+ */
+mla_status_t mla_accumulate_weights_fp8(
+    const void* q, const float* lse, const void* blocks, const float* scales,
+    const uint32_t* cache_lengths, const uint32_t* lookup_table, const uint32_t* scales_lookup_table,
+    uint32_t max_prompt_length, uint32_t max_cache_length, uint32_t layer_idx, float softmax_scale,
+    const mla_paged_shape_t* shape, const float* scores, int64_t scores_stride,
+    float* out, int64_t out_stride, cudaStream_t stream);
+
+/*
+ * mla_select_keys -- the keys each request keeps.  Request b holds lengths[b] keys with weights
+ * scores[b][0 .. lengths[b]).  If lengths[b] <= budget it keeps all of them.  Otherwise it keeps its
+ * first num_sink keys, its last num_recent keys and, of the keys between, the
+ * budget - num_sink - num_recent with the largest weights: equal weights go to the lowest index, -0
+ * equals +0, and NaN ranks below every number.  kept[b][0 .. kept_lengths[b]) receives the indices,
+ * strictly ascending; later entries are left as they were.  kept_lengths[b] = min(lengths[b], budget).
+ *
+ *   scores        fp32, row b at scores + b * scores_stride (scores_stride >= max_length)
+ *   lengths       uint32 [batch] device; max_length >= every length (host scalar; a larger length is
+ *                 clamped to it and flagged, MLA_ERR_DEVICE_BOUNDS)
+ *   budget        >= 1; num_recent, num_sink >= 0 with num_recent + num_sink <= budget
+ *   kept          int32, row b at kept + b * kept_stride (kept_stride >= min(budget, max_length))
+ *   kept_lengths  int32 [batch], written
+ * No workspace; batch = 0 is a no-op.
+ */
+mla_status_t mla_select_keys(
+    const float* scores, int64_t scores_stride, const uint32_t* lengths, int32_t batch, uint32_t max_length,
+    int32_t budget, int32_t num_recent, int32_t num_sink, int32_t* kept, int64_t kept_stride,
+    int32_t* kept_lengths, cudaStream_t stream);
+
+/*
+ * mla_compact_paged -- moves, in place and for one layer, row kept[b][j] of request b to row j for
+ * j < kept_lengths[b]: the cache row of every kv plane, its scales and its accumulated weight.  kept
+ * must be strictly ascending (as mla_select_keys writes it), so that tokens keep their order; rows at
+ * kept_lengths[b] and behind keep what they held.  Requests must not share pages in which rows move.
+ *
+ *   kept, kept_lengths    int32; row b at kept + b * kept_stride, at most max_kept entries read
+ *   lookup_table, scales_lookup_table, layer_idx   as for mla_decode_paged_fp8
+ *   element_bytes         1 (e4m3 codes) or 2 (bf16) per element of blocks
+ *   shape                 batch, num_blocks, kv_dim, num_layers, page_size (any), num_kv_heads,
+ *                         head_dim, num_scale_blocks, head_dim_granularity (any) and max_pages; a
+ *                         token's row, num_kv_heads * head_dim * element_bytes, is a multiple of 32
+ *   blocks                16-byte aligned; scales fp32 or NULL (none); both written in place
+ *   scores                fp32 or NULL: row b at scores + b * scores_stride, scores_cols values long
+ * No workspace.  A kept index that is below its own position, or whose position or source has no page
+ * (or, for the weights, is not below scores_cols), is skipped and flagged (MLA_ERR_DEVICE_BOUNDS).
+ */
+mla_status_t mla_compact_paged(
+    const int32_t* kept, int64_t kept_stride, int32_t max_kept, const int32_t* kept_lengths,
+    const uint32_t* lookup_table, const uint32_t* scales_lookup_table, uint32_t layer_idx,
+    int32_t element_bytes, const mla_paged_shape_t* shape, void* blocks, float* scales,
+    float* scores, int64_t scores_stride, int32_t scores_cols, cudaStream_t stream);
+
+/*
+ * The multi-head cache: the same 6-D paged layout with keys in kv plane 0 and values in plane 1
+ * (kv_dim >= 2), num_kv_heads heads of head_dim values, as bf16 (element_bytes 2, scales NULL) or e4m3
+ * (element_bytes 1) with one fp32 scale per token and head: scales [num_scale_blocks, kv_dim,
+ * num_layers, page_size, num_kv_heads, 1].  Implemented subset: head_dim 64 or 128,
+ * head_dim_granularity 1, page_size a multiple of 16, num_kv_heads <= 256 (v_dim is not read).
+ *
+ * mla_mha_kv_store -- writes the step's keys and values: new token i of request b goes to position
+ * cache_lengths[b] + i.  bf16 rows are copied; for e4m3, each token's head row x gets
+ * scale = f32(max |x|) / 448 rounded to fp32 (1.0 for an all-zero row) and codes
+ * e4m3 of f32(x_d / scale), round to nearest even, saturated (the recipe of mla_kv_store_fp8).
+ * Non-finite inputs are not supported for e4m3.
+ *
+ *   k, v    bf16 [batch, num_new_tokens, num_kv_heads, head_dim], 16-byte aligned
+ * Other arguments, bad pages and no-ops as for mla_kv_store_fp8.
+ */
+mla_status_t mla_mha_kv_store(
+    const void* k, const void* v, const uint32_t* cache_lengths, const uint32_t* lookup_table,
+    const uint32_t* scales_lookup_table, uint32_t num_new_tokens, uint32_t layer_idx, int32_t element_bytes,
+    const mla_paged_shape_t* shape, void* blocks, float* scales, cudaStream_t stream);
+
+/*
+ * mla_mha_decode_paged -- decode attention over the multi-head cache, with grouped queries: query head
+ * h reads kv head h / (num_q_heads / num_kv_heads).  For request b and query token i,
+ *     x[t] = softmax_scale <q[b,i,h,:], K[t]> for t <= cache_lengths[b] + i,
+ *     lse  = ln sum_t exp(x[t]),  out[b,i,h,:] = sum_t exp(x[t] - lse) V[t],
+ * with K and V the stored bf16 values, or e4m3 * scale unrounded.  Keys, values and scales of the
+ * stored tokens are to be finite; what the cache holds behind a request's end is never used.
+ *
+ *   q          bf16 [batch, max_prompt_length, num_q_heads, head_dim], 16-byte aligned
+ *   out        bf16, as q; lse fp32 [batch, max_prompt_length, num_q_heads], natural log, or NULL
+ *   workspace  device memory of at least mla_mha_decode_workspace_bytes bytes (0 for short caches:
+ *              then NULL may be passed), 16-byte aligned, for the partial results of requests that are
+ *              split over SMs.  It is the caller's: calls that overlap on the device, or captured
+ *              graphs that are replayed at the same time, need one each.  Nothing in it has to start
+ *              at zero and nothing is kept in it from call to call.
+ * Other arguments as for mla_decode_paged_fp8.  Errors as there, and MLA_ERR_WORKSPACE where the
+ * workspace is missing or too small.  A page id past the pool leaves its keys out and is flagged.
+ */
+mla_status_t mla_mha_decode_paged(
+    const void* q, const void* blocks, const float* scales,
+    const uint32_t* cache_lengths, const uint32_t* lookup_table, const uint32_t* scales_lookup_table,
+    uint32_t max_prompt_length, uint32_t max_cache_length, uint32_t layer_idx, float softmax_scale,
+    int32_t element_bytes, const mla_paged_shape_t* shape, void* out, float* lse,
+    void* workspace, uint64_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace that mla_mha_decode_paged needs for these arguments on the current device. */
+mla_status_t mla_mha_decode_workspace_bytes(
+    uint32_t max_prompt_length, uint32_t max_cache_length, int32_t element_bytes,
+    const mla_paged_shape_t* shape, uint64_t* bytes);
+
+/*
  * mla_set_num_clusters -- test and tuning hook: fix the number of 2-CTA clusters
  * the decode splits the keys over (0 restores the default, one per resident
  * cluster slot of the device).  Process-wide.  Smaller values make fewer, longer

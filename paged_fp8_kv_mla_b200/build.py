@@ -16,7 +16,7 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = [os.path.join(PKG, "csrc", "mla_api.cu")]
+SRC = [os.path.join(PKG, "csrc", "mla_lib.cu")]
 def _deps():
     """Every source the library is built from (all of csrc/ and the public header)."""
     d = os.path.join(PKG, "csrc")

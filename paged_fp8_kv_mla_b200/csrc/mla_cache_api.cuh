@@ -1,0 +1,518 @@
+// Host side of the cache operators' C ABI: eviction from the latent cache (accumulated weights,
+// selection, compaction) and the multi-head cache (KV-store step, decode).  Part of the library's
+// one translation unit (mla_lib.cu), after the decode's host side, whose helpers it uses.
+#pragma once
+#include "mla_accumulate.cuh"
+#include "mla_compact.cuh"
+#include "mla_mha_decode.cuh"
+#include "mla_mha_store.cuh"
+#include "mla_select.cuh"
+
+namespace {
+
+int gcd_int(int a, int b) { return b == 0 ? a : gcd_int(b, a % b); }
+
+// Current device, its SM count, and (once per device) the shared-memory limits of the kernels here.
+mla_status_t cache_device(int* sms) {
+  static int g_sms[kMaxDevices];
+  int dev = 0;
+  MLA_CUDA(cudaGetDevice(&dev));
+  if (dev >= kMaxDevices) return fail(MLA_ERR_UNSUPPORTED, "device index too large");
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_sms[dev] == 0) {
+    int n = 0;
+    MLA_CUDA(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev));
+    auto smem = [](auto* kernel, size_t bytes) {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    };
+    MLA_CUDA(smem(mla::mla_accumulate_kernel, mla::ACC_SMEM_ALLOC));
+    MLA_CUDA(smem(mla::mla_select_kernel, mla::SEL_KEYS_OFF + mla::SEL_CACHE * 4));
+    MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, false>, mla::MHA_SMEM_LIMIT));
+    MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, true>, mla::MHA_SMEM_LIMIT));
+    MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, false>, mla::MHA_SMEM_LIMIT));
+    MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, true>, mla::MHA_SMEM_LIMIT));
+    g_sms[dev] = n;
+  }
+  *sms = g_sms[dev];
+  return MLA_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A paged array's pool and page-table description, for any row width; the latent cache's own checks
+// (check_cache) go further.
+mla_status_t check_pages(const mla_paged_shape_t* s, uint32_t layer_idx) {
+  if (s->batch < 0 || s->num_blocks < 1 || s->kv_dim < 1 || s->num_layers < 1 || s->page_size < 1 ||
+      s->num_kv_heads < 1 || s->head_dim < 1 || s->num_scale_blocks < 1 || s->head_dim_granularity < 1 || s->max_pages < 1)
+    return fail(MLA_ERR_INVALID_ARG, "non-positive dimension in shape");
+  if (layer_idx >= static_cast<uint32_t>(s->num_layers))
+    return fail(MLA_ERR_INVALID_ARG, "layer_idx %u >= num_layers %d", layer_idx, s->num_layers);
+  const double rows = static_cast<double>(s->num_blocks) * s->kv_dim * s->num_layers * s->page_size;
+  const double srows = static_cast<double>(s->num_scale_blocks) * s->kv_dim * s->num_layers * s->page_size;
+  if (rows >= 2147483648.0 || srows >= 2147483648.0)
+    return fail(MLA_ERR_UNSUPPORTED, "block pool too large (%.0f rows)", rows > srows ? rows : srows);
+  if (static_cast<double>(s->max_pages) * s->page_size >= 1073741824.0)
+    return fail(MLA_ERR_UNSUPPORTED, "max_pages * page_size too large");
+  return MLA_OK;
+}
+
+// The multi-head cache: kv plane 0 keys, plane 1 values, head_dim 64 or 128, bf16 or e4m3 with one scale
+// per token and head.
+mla_status_t check_mha(const mla_paged_shape_t* s, uint32_t layer_idx, int32_t element_bytes, const void* blocks,
+                       const void* scales, const uint32_t* cache_lengths, const uint32_t* lookup_table) {
+  if (!s) return fail(MLA_ERR_INVALID_ARG, "shape is NULL");
+  if (!blocks || !cache_lengths || !lookup_table)
+    return fail(MLA_ERR_INVALID_ARG, "blocks, cache_lengths and lookup_table must be non-NULL");
+  const mla_status_t st = check_pages(s, layer_idx);
+  if (st != MLA_OK) return st;
+  if (element_bytes != 1 && element_bytes != 2)
+    return fail(MLA_ERR_INVALID_ARG, "element_bytes must be 1 (e4m3) or 2 (bf16), got %d", element_bytes);
+  if ((element_bytes == 1) != (scales != nullptr))
+    return fail(MLA_ERR_INVALID_ARG, "an e4m3 cache needs scales and a bf16 cache takes none");
+  if (s->head_dim != 64 && s->head_dim != 128)
+    return fail(MLA_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", s->head_dim);
+  if (s->kv_dim < 2) return fail(MLA_ERR_INVALID_ARG, "kv_dim must be at least 2 (keys and values)");
+  if (s->num_kv_heads > 256) return fail(MLA_ERR_UNSUPPORTED, "num_kv_heads must be at most 256 (got %d)", s->num_kv_heads);
+  if (s->head_dim_granularity != 1)
+    return fail(MLA_ERR_UNSUPPORTED, "only one scale per token and head (head_dim_granularity 1) is implemented");
+  if (s->page_size % 16 != 0) return fail(MLA_ERR_UNSUPPORTED, "page_size must be a multiple of 16");
+  if (!aligned16(blocks) || !aligned16(scales)) return fail(MLA_ERR_INVALID_ARG, "blocks and scales must be 16-byte aligned");
+  return MLA_OK;
+}
+
+// blocks as {column bytes, rows, columns}: one box = `cols` columns of `box_rows` rows.
+mla_status_t make_row_map(CUtensorMap* map, const void* blocks, uint64_t rows, uint64_t row_bytes, int col_bytes,
+                          int box_rows, int cols) {
+  EncodeTiledFn enc = nullptr;
+  const mla_status_t st = get_encode_fn(&enc);
+  if (st != MLA_OK) return st;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(col_bytes), rows, row_bytes / col_bytes};
+  const cuuint64_t strides[2] = {row_bytes, static_cast<cuuint64_t>(col_bytes)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(col_bytes), static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(cols)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(blocks), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, col_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled(blocks) failed (%d)", static_cast<int>(r));
+  return MLA_OK;
+}
+
+// How a multi-head decode is laid out (the rules the kernel's header comment describes).
+struct MhaPlan {
+  int R, hg, mt, kw, head_groups, row_groups, tile, box_rows, stages, NC, one_item;
+  uint32_t plane_bytes, stage_bytes, smem;
+  uint64_t part_lse_off, desc_off, total;
+};
+
+mla_status_t mha_plan(const mla_paged_shape_t* s, uint32_t T, uint32_t max_cache_length, int element_bytes, int sms,
+                      MhaPlan* out) {
+  MhaPlan m{};
+  if (s->num_q_heads < 1 || s->num_q_heads % s->num_kv_heads != 0)
+    return fail(MLA_ERR_INVALID_ARG, "num_q_heads %d must be a positive multiple of num_kv_heads %d", s->num_q_heads,
+                s->num_kv_heads);
+  if (T < 1) return fail(MLA_ERR_INVALID_ARG, "max_prompt_length must be >= 1");
+  if (static_cast<uint64_t>(max_cache_length) + T + 256 >= (1ull << 30))
+    return fail(MLA_ERR_UNSUPPORTED, "max_cache_length too large");
+  const uint64_t need = (static_cast<uint64_t>(max_cache_length) + T + s->page_size - 1) / s->page_size;
+  if (need > static_cast<uint64_t>(s->max_pages))
+    return fail(MLA_ERR_INVALID_ARG, "lookup_table has %d pages per request, %llu needed for max_cache_length %u",
+                s->max_pages, static_cast<unsigned long long>(need), max_cache_length);
+  const uint64_t R = static_cast<uint64_t>(T) * (s->num_q_heads / s->num_kv_heads);
+  if (R > (1u << 24)) return fail(MLA_ERR_UNSUPPORTED, "too many query rows per kv head");
+  m.R = static_cast<int>(R);
+  // Warps: first the row tiles of a head (they share its keys), then heads, then the keys of a tile.
+  const int row_tiles = (m.R + 15) / 16;
+  m.mt = row_tiles < mla::MHA_WARPS ? row_tiles : mla::MHA_WARPS;
+  m.row_groups = (row_tiles + m.mt - 1) / m.mt;
+  const int most = mla::MHA_WARPS / m.mt;
+  m.head_groups = (s->num_kv_heads + most - 1) / most;
+  m.hg = (s->num_kv_heads + m.head_groups - 1) / m.head_groups;
+  m.kw = 1;
+  while (2 * m.kw * m.hg * m.mt <= mla::MHA_WARPS) m.kw *= 2;
+  // Tile: 16 keys per warp, doubled while a ring stage stays within 32 KB.
+  const uint32_t per_key = 2u * m.hg * s->head_dim * element_bytes + (element_bytes == 1 ? 8u * s->num_kv_heads : 0u);
+  m.tile = 16 * m.kw;
+  while (m.tile < 128 && 2 * m.tile * per_key <= 32768) m.tile *= 2;
+  m.box_rows = gcd_int(s->page_size, m.tile);
+  m.plane_bytes = static_cast<uint32_t>(m.tile) * m.hg * s->head_dim * element_bytes;
+  m.stage_bytes = static_cast<uint32_t>(align_up(m.tile * per_key, 1024));
+  const uint32_t merge = m.kw > 1 ? (s->head_dim == 64 ? mla::mha_merge_bytes<64>() : mla::mha_merge_bytes<128>()) : 0;
+  const uint32_t rest = merge + mla::MHA_MISC_BYTES + 1024;
+  m.stages = static_cast<int>((mla::MHA_SMEM_LIMIT - rest) / m.stage_bytes);
+  if (m.stages > mla::MHA_MAX_STAGES) m.stages = mla::MHA_MAX_STAGES;
+  if (m.stages < 2) return fail(MLA_ERR_UNSUPPORTED, "%d kv heads: a tile's scales do not fit shared memory", s->num_kv_heads);
+  m.smem = m.stages * m.stage_bytes + rest;
+  const uint64_t items = static_cast<uint64_t>(s->batch) * m.head_groups * m.row_groups;
+  const uint64_t max_tiles = (static_cast<uint64_t>(max_cache_length) + T + m.tile - 1) / m.tile;
+  if (items > 0x7FFFFFFFull) return fail(MLA_ERR_UNSUPPORTED, "too many (request, head group, row group) items");
+  // Items of a few tiles are not worth cutting: one CTA each, and no second launch.
+  m.one_item = max_tiles <= 4;
+  const uint64_t most_tiles = items * max_tiles;
+  m.NC = m.one_item ? static_cast<int>(items) : static_cast<int>(most_tiles < static_cast<uint64_t>(sms) ? most_tiles : sms);
+  if (!m.one_item) {
+    uint64_t o = align_up(sizeof(float) * 2ull * m.NC * mla::MHA_ROWS * s->head_dim, 256);
+    m.part_lse_off = o;
+    o = align_up(o + sizeof(float) * 2ull * m.NC * mla::MHA_ROWS, 256);
+    m.desc_off = o;
+    m.total = align_up(o + sizeof(int4) * m.NC, 256);
+  }
+  *out = m;
+  return MLA_OK;
+}
+
+template <int D, bool FP8>
+mla_status_t mha_launch(const mla::MhaParams& p, const MhaPlan& m, cudaStream_t stream) {
+  mla::mla_mha_decode_kernel<D, FP8><<<m.NC, mla::MHA_THREADS, m.smem, stream>>>(p);
+  MLA_CUDA(cudaGetLastError());
+  if (m.one_item) return MLA_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(m.NC, static_cast<unsigned>((m.hg * m.mt * 16 + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  MLA_CUDA(cudaLaunchKernelEx(&cfg, mla::mla_mha_join_kernel<D>, p));
+  return MLA_OK;
+}
+
+template <int D, bool FP8>
+mla_status_t mha_store_launch(const mla::MhaStoreParams& p, cudaStream_t stream) {
+  const uint64_t per_cta = mla::MST_THREADS / (D / 8);
+  const uint64_t grid = (p.rows + per_cta - 1) / per_cta;
+  mla::mla_mha_store_kernel<D, FP8><<<dim3(static_cast<unsigned>(grid), 2), mla::MST_THREADS, 0, stream>>>(p);
+  MLA_CUDA(cudaGetLastError());
+  return MLA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status_t mla_accumulate_weights_fp8(const void* q, const float* lse, const void* blocks, const float* scales,
+                                        const uint32_t* cache_lengths, const uint32_t* lookup_table,
+                                        const uint32_t* scales_lookup_table, uint32_t max_prompt_length,
+                                        uint32_t max_cache_length, uint32_t layer_idx, float softmax_scale,
+                                        const mla_paged_shape_t* shape, const float* scores, int64_t scores_stride,
+                                        float* out, int64_t out_stride, cudaStream_t stream) {
+  mla::DecodeParams d{};
+  uint64_t rows = 0;
+  mla_status_t st = check_cache(blocks, scales, cache_lengths, lookup_table, max_prompt_length, max_cache_length,
+                                layer_idx, shape, &d, &rows);
+  if (st != MLA_OK) return st;
+  if (d.SG != 1)
+    return fail(MLA_ERR_UNSUPPORTED, "the accumulated weights take one scale per token (head_dim_granularity 1)");
+  if (!q || !lse || !out) return fail(MLA_ERR_INVALID_ARG, "q, lse and out must be non-NULL");
+  if (!aligned16(q)) return fail(MLA_ERR_INVALID_ARG, "q must be 16-byte aligned");
+  if (!aligned4(lse) || !aligned4(scores) || !aligned4(out))
+    return fail(MLA_ERR_INVALID_ARG, "lse, scores and out must be 4-byte aligned");
+  if (!(softmax_scale == softmax_scale)) return fail(MLA_ERR_INVALID_ARG, "softmax_scale is NaN");
+  const int64_t need = static_cast<int64_t>(max_cache_length) + max_prompt_length;
+  if (out_stride < need || (scores && scores_stride < need))
+    return fail(MLA_ERR_INVALID_ARG, "the rows of scores and out must hold max_cache_length + max_prompt_length = %lld values",
+                static_cast<long long>(need));
+  if (d.B == 0) return MLA_OK;
+  if (static_cast<int64_t>(d.T) * d.G > 0x3FFFFFFF) return fail(MLA_ERR_UNSUPPORTED, "too many query tokens");
+  int sms = 0;
+  st = cache_device(&sms);
+  if (st != MLA_OK) return st;
+  mla::AccumulateParams p{};
+  p.box_rows = gcd_int(d.P, mla::ACC_BN);
+  st = make_row_map(&p.tmap_k, blocks, rows, mla::HEAD_DIM, 64, p.box_rows, 1);
+  if (st != MLA_OK) return st;
+  p.q = static_cast<const uint16_t*>(q);
+  p.lse = lse;
+  p.scales = scales;
+  p.cache_lengths = cache_lengths;
+  p.lut = lookup_table;
+  p.slut = scales_lookup_table;
+  p.scores = scores;
+  p.out = out;
+  p.scores_stride = scores_stride;
+  p.out_stride = out_stride;
+  p.status = status_ptr();
+  if (!p.status) return fail(MLA_ERR_CUDA, "status word address unavailable");
+  p.B = d.B;
+  p.T = d.T;
+  p.H = d.H;
+  p.G = d.G;
+  p.P = d.P;
+  p.KVD = d.KVD;
+  p.NL = d.NL;
+  p.layer = d.layer;
+  p.NB = d.NB;
+  p.NSB = d.NSB;
+  p.max_pages = d.max_pages;
+  p.max_cache_length = max_cache_length;
+  p.divP = d.divP;
+  p.divG = d.divG;
+  p.softmax_scale = softmax_scale;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    p.wait_limit_ns = g_wait_limit_ns;
+  }
+  const uint64_t most = static_cast<uint64_t>(d.B) * ((need + mla::ACC_BN - 1) / mla::ACC_BN);
+  const unsigned grid = static_cast<unsigned>(most < static_cast<uint64_t>(sms) ? most : sms);
+  mla::mla_accumulate_kernel<<<grid, mla::ACC_THREADS, mla::ACC_SMEM_ALLOC, stream>>>(p);
+  MLA_CUDA(cudaGetLastError());
+  return MLA_OK;
+}
+
+mla_status_t mla_select_keys(const float* scores, int64_t scores_stride, const uint32_t* lengths, int32_t batch,
+                             uint32_t max_length, int32_t budget, int32_t num_recent, int32_t num_sink, int32_t* kept,
+                             int64_t kept_stride, int32_t* kept_lengths, cudaStream_t stream) {
+  if (batch < 0 || num_recent < 0 || num_sink < 0) return fail(MLA_ERR_INVALID_ARG, "batch, num_recent and num_sink must be >= 0");
+  if (budget < 1) return fail(MLA_ERR_INVALID_ARG, "budget must be >= 1");
+  if (static_cast<int64_t>(num_recent) + num_sink > budget)
+    return fail(MLA_ERR_INVALID_ARG, "num_recent %d + num_sink %d exceed the budget %d", num_recent, num_sink, budget);
+  if (!scores || !lengths || !kept || !kept_lengths)
+    return fail(MLA_ERR_INVALID_ARG, "scores, lengths, kept and kept_lengths must be non-NULL");
+  if (!aligned4(scores) || !aligned4(kept)) return fail(MLA_ERR_INVALID_ARG, "scores and kept must be 4-byte aligned");
+  if (max_length >= (1u << 30)) return fail(MLA_ERR_UNSUPPORTED, "max_length too large");
+  if (scores_stride < static_cast<int64_t>(max_length))
+    return fail(MLA_ERR_INVALID_ARG, "the rows of scores must hold max_length = %u values", max_length);
+  const int64_t most = budget < static_cast<int64_t>(max_length) ? budget : static_cast<int64_t>(max_length);
+  if (kept_stride < most) return fail(MLA_ERR_INVALID_ARG, "the rows of kept must hold %lld values", static_cast<long long>(most));
+  if (batch == 0) return MLA_OK;
+  int sms = 0;
+  mla_status_t st = cache_device(&sms);
+  if (st != MLA_OK) return st;
+  mla::SelectParams p{};
+  p.scores = scores;
+  p.lengths = lengths;
+  p.kept = kept;
+  p.kept_lengths = kept_lengths;
+  p.status = status_ptr();
+  if (!p.status) return fail(MLA_ERR_CUDA, "status word address unavailable");
+  p.scores_stride = scores_stride;
+  p.kept_stride = kept_stride;
+  p.max_length = max_length;
+  p.budget = budget;
+  p.recent = num_recent;
+  p.sink = num_sink;
+  // CTAs per request: about 2048 keys each, up to the portable cluster size.
+  int ncta = 1;
+  while (ncta < 8 && static_cast<uint32_t>(ncta) * 2048 < max_length) ncta *= 2;
+  if (static_cast<int64_t>(batch) * ncta > 0x7FFFFFFF) return fail(MLA_ERR_UNSUPPORTED, "batch too large");
+  const uint32_t per = (max_length + ncta - 1) / ncta;
+  const uint32_t cached = per < static_cast<uint32_t>(mla::SEL_CACHE) ? per : mla::SEL_CACHE;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(batch) * ncta);
+  cfg.blockDim = dim3(mla::SEL_THREADS);
+  cfg.dynamicSmemBytes = mla::SEL_KEYS_OFF + cached * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ncta;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  MLA_CUDA(cudaLaunchKernelEx(&cfg, mla::mla_select_kernel, p));
+  return MLA_OK;
+}
+
+mla_status_t mla_compact_paged(const int32_t* kept, int64_t kept_stride, int32_t max_kept, const int32_t* kept_lengths,
+                               const uint32_t* lookup_table, const uint32_t* scales_lookup_table, uint32_t layer_idx,
+                               int32_t element_bytes, const mla_paged_shape_t* s, void* blocks, float* scales,
+                               float* scores, int64_t scores_stride, int32_t scores_cols, cudaStream_t stream) {
+  if (!s) return fail(MLA_ERR_INVALID_ARG, "shape is NULL");
+  if (!kept || !kept_lengths || !lookup_table || !blocks)
+    return fail(MLA_ERR_INVALID_ARG, "kept, kept_lengths, lookup_table and blocks must be non-NULL");
+  mla_status_t st = check_pages(s, layer_idx);
+  if (st != MLA_OK) return st;
+  if (element_bytes != 1 && element_bytes != 2)
+    return fail(MLA_ERR_INVALID_ARG, "element_bytes must be 1 (e4m3) or 2 (bf16), got %d", element_bytes);
+  if (max_kept < 1 || kept_stride < max_kept) return fail(MLA_ERR_INVALID_ARG, "max_kept must be >= 1 and at most kept_stride");
+  if (!aligned16(blocks)) return fail(MLA_ERR_INVALID_ARG, "blocks must be 16-byte aligned");
+  if (!aligned4(scales) || !aligned4(scores)) return fail(MLA_ERR_INVALID_ARG, "scales and scores must be 4-byte aligned");
+  const int64_t row_bytes = static_cast<int64_t>(s->num_kv_heads) * s->head_dim * element_bytes;
+  const int64_t row_words = static_cast<int64_t>(s->num_kv_heads) * s->head_dim_granularity;
+  if (row_bytes % 32 != 0 || row_bytes > (1 << 20))
+    return fail(MLA_ERR_UNSUPPORTED, "a token's row (%lld bytes) must be a multiple of 32 bytes, at most 1 MB",
+                static_cast<long long>(row_bytes));
+  if (static_cast<int64_t>(max_kept) * row_words >= (1ll << 30) || max_kept >= (1 << 28))
+    return fail(MLA_ERR_UNSUPPORTED, "too many rows to move");
+  if (scores && (scores_cols < 1 || scores_stride < scores_cols))
+    return fail(MLA_ERR_INVALID_ARG, "scores_cols must be >= 1 and at most scores_stride");
+  if (s->batch == 0) return MLA_OK;
+  if (s->batch > 65535) return fail(MLA_ERR_UNSUPPORTED, "batch must be at most 65535");
+  int sms = 0;
+  st = cache_device(&sms);
+  if (st != MLA_OK) return st;
+  mla::CompactParams p{};
+  p.kept = kept;
+  p.kept_lengths = kept_lengths;
+  p.lut = lookup_table;
+  p.slut = scales_lookup_table ? scales_lookup_table : lookup_table;
+  p.blocks = static_cast<uint8_t*>(blocks);
+  p.scales = scales;
+  p.scores = scores;
+  p.status = status_ptr();
+  if (!p.status) return fail(MLA_ERR_CUDA, "status word address unavailable");
+  p.kept_stride = kept_stride;
+  p.scores_stride = scores_stride;
+  p.max_kept = max_kept;
+  p.scores_cols = scores_cols;
+  p.P = s->page_size;
+  p.KVD = s->kv_dim;
+  p.NL = s->num_layers;
+  p.layer = static_cast<int>(layer_idx);
+  p.NB = s->num_blocks;
+  p.NSB = s->num_scale_blocks;
+  p.max_pages = s->max_pages;
+  p.row_bytes = static_cast<int>(row_bytes);
+  p.row_words = static_cast<int>(row_words);
+  p.divP = make_fastdiv(static_cast<uint32_t>(s->page_size));
+  p.divW = make_fastdiv(static_cast<uint32_t>(row_words));
+  // 64-byte slices where they already give every SM a CTA, else 32-byte slices (a DRAM sector)
+  const bool narrow = row_bytes % 64 != 0 || static_cast<int64_t>(s->batch) * s->kv_dim * (row_bytes / 64) < sms;
+  p.slices = static_cast<int>(row_bytes / (narrow ? 32 : 64));
+  const int64_t gx = static_cast<int64_t>(s->kv_dim) * (p.slices + 1) + 1;
+  if (gx > 0x7FFFFFFF) return fail(MLA_ERR_UNSUPPORTED, "grid too large");
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(s->batch));
+  if (narrow)
+    mla::mla_compact_kernel<32><<<grid, mla::CMP_THREADS, 0, stream>>>(p);
+  else
+    mla::mla_compact_kernel<64><<<grid, mla::CMP_THREADS, 0, stream>>>(p);
+  MLA_CUDA(cudaGetLastError());
+  return MLA_OK;
+}
+
+mla_status_t mla_mha_kv_store(const void* k, const void* v, const uint32_t* cache_lengths, const uint32_t* lookup_table,
+                              const uint32_t* scales_lookup_table, uint32_t num_new_tokens, uint32_t layer_idx,
+                              int32_t element_bytes, const mla_paged_shape_t* s, void* blocks, float* scales,
+                              cudaStream_t stream) {
+  mla_status_t st = check_mha(s, layer_idx, element_bytes, blocks, scales, cache_lengths, lookup_table);
+  if (st != MLA_OK) return st;
+  mla::MhaStoreParams p{};
+  p.rows = static_cast<uint64_t>(s->batch) * num_new_tokens * s->num_kv_heads;
+  if (p.rows == 0) return MLA_OK;
+  if (!k || !v) return fail(MLA_ERR_INVALID_ARG, "k and v must be non-NULL");
+  if (!aligned16(k) || !aligned16(v)) return fail(MLA_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+  if (static_cast<uint64_t>(s->batch) * num_new_tokens >= (1ull << 31) || p.rows >= (1ull << 31))
+    return fail(MLA_ERR_UNSUPPORTED, "too many new rows (%llu)", p.rows);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.cache_lengths = cache_lengths;
+  p.lut = lookup_table;
+  p.slut = scales_lookup_table;
+  p.blocks = static_cast<uint8_t*>(blocks);
+  p.scales = scales;
+  p.status = status_ptr();
+  if (!p.status) return fail(MLA_ERR_CUDA, "status word address unavailable");
+  p.B = s->batch;
+  p.T = static_cast<int>(num_new_tokens);
+  p.HKV = s->num_kv_heads;
+  p.P = s->page_size;
+  p.KVD = s->kv_dim;
+  p.NL = s->num_layers;
+  p.layer = static_cast<int>(layer_idx);
+  p.NB = s->num_blocks;
+  p.NSB = s->num_scale_blocks;
+  p.max_pages = s->max_pages;
+  p.divH = make_fastdiv(static_cast<uint32_t>(p.HKV));
+  p.divT = make_fastdiv(num_new_tokens);
+  if (s->head_dim == 64)
+    return element_bytes == 1 ? mha_store_launch<64, true>(p, stream) : mha_store_launch<64, false>(p, stream);
+  return element_bytes == 1 ? mha_store_launch<128, true>(p, stream) : mha_store_launch<128, false>(p, stream);
+}
+
+mla_status_t mla_mha_decode_workspace_bytes(uint32_t max_prompt_length, uint32_t max_cache_length, int32_t element_bytes,
+                                            const mla_paged_shape_t* s, uint64_t* bytes) {
+  if (!s || !bytes) return fail(MLA_ERR_INVALID_ARG, "shape and bytes must be non-NULL");
+  *bytes = 0;
+  mla_status_t st = check_pages(s, 0);
+  if (st != MLA_OK) return st;
+  if (s->batch == 0) return MLA_OK;
+  int sms = 0;
+  st = cache_device(&sms);
+  if (st != MLA_OK) return st;
+  MhaPlan m{};
+  st = mha_plan(s, max_prompt_length, max_cache_length, element_bytes, sms, &m);
+  if (st == MLA_OK) *bytes = m.total;
+  return st;
+}
+
+mla_status_t mla_mha_decode_paged(const void* q, const void* blocks, const float* scales, const uint32_t* cache_lengths,
+                                  const uint32_t* lookup_table, const uint32_t* scales_lookup_table,
+                                  uint32_t max_prompt_length, uint32_t max_cache_length, uint32_t layer_idx,
+                                  float softmax_scale, int32_t element_bytes, const mla_paged_shape_t* s, void* out,
+                                  float* lse, void* workspace, uint64_t workspace_bytes, cudaStream_t stream) {
+  mla_status_t st = check_mha(s, layer_idx, element_bytes, blocks, scales, cache_lengths, lookup_table);
+  if (st != MLA_OK) return st;
+  if (!q || !out) return fail(MLA_ERR_INVALID_ARG, "q and out must be non-NULL");
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace))
+    return fail(MLA_ERR_INVALID_ARG, "q, out and workspace must be 16-byte aligned");
+  if (!aligned4(lse)) return fail(MLA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  if (!(softmax_scale == softmax_scale)) return fail(MLA_ERR_INVALID_ARG, "softmax_scale is NaN");
+  MhaPlan m{};
+  if (s->batch == 0) return mha_plan(s, max_prompt_length, max_cache_length, element_bytes, 1, &m);
+  int sms = 0;
+  st = cache_device(&sms);
+  if (st != MLA_OK) return st;
+  st = mha_plan(s, max_prompt_length, max_cache_length, element_bytes, sms, &m);
+  if (st != MLA_OK) return st;
+  if (m.total > 0 && (!workspace || workspace_bytes < m.total))
+    return fail(MLA_ERR_WORKSPACE, "the call needs a workspace of %llu bytes (mla_mha_decode_workspace_bytes)",
+                static_cast<unsigned long long>(m.total));
+  mla::MhaParams p{};
+  const uint64_t rows = static_cast<uint64_t>(s->num_blocks) * s->kv_dim * s->num_layers * s->page_size;
+  const int head_bytes = s->head_dim * element_bytes, col = head_bytes < 128 ? head_bytes : 128;
+  st = make_row_map(&p.tmap, blocks, rows, static_cast<uint64_t>(s->num_kv_heads) * head_bytes, col, m.box_rows,
+                    m.hg * (head_bytes / col));
+  if (st != MLA_OK) return st;
+  p.q = static_cast<const uint16_t*>(q);
+  p.scales = scales;
+  p.cache_lengths = cache_lengths;
+  p.lut = lookup_table;
+  p.slut = scales_lookup_table ? scales_lookup_table : lookup_table;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  if (m.total > 0) {
+    char* w = static_cast<char*>(workspace);
+    p.part_o = reinterpret_cast<float*>(w);
+    p.part_lse = reinterpret_cast<float*>(w + m.part_lse_off);
+    p.desc = reinterpret_cast<int4*>(w + m.desc_off);
+  }
+  p.status = status_ptr();
+  if (!p.status) return fail(MLA_ERR_CUDA, "status word address unavailable");
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    p.wait_limit_ns = g_wait_limit_ns;
+  }
+  p.B = s->batch;
+  p.T = static_cast<int>(max_prompt_length);
+  p.H = s->num_q_heads;
+  p.HKV = s->num_kv_heads;
+  p.R = m.R;
+  p.P = s->page_size;
+  p.KVD = s->kv_dim;
+  p.NL = s->num_layers;
+  p.layer = static_cast<int>(layer_idx);
+  p.NB = s->num_blocks;
+  p.NSB = s->num_scale_blocks;
+  p.max_pages = s->max_pages;
+  p.max_cache_length = max_cache_length;
+  p.hg = m.hg;
+  p.mt = m.mt;
+  p.kw = m.kw;
+  p.head_groups = m.head_groups;
+  p.row_groups = m.row_groups;
+  p.tile = m.tile;
+  p.box_rows = m.box_rows;
+  p.stages = m.stages;
+  p.plane_bytes = m.plane_bytes;
+  p.stage_bytes = m.stage_bytes;
+  p.one_item = m.one_item;
+  p.divP = make_fastdiv(static_cast<uint32_t>(p.P));
+  p.divG = make_fastdiv(static_cast<uint32_t>(s->num_q_heads / s->num_kv_heads));
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  if (s->head_dim == 64)
+    return element_bytes == 1 ? mha_launch<64, true>(p, m, stream) : mha_launch<64, false>(p, m, stream);
+  return element_bytes == 1 ? mha_launch<128, true>(p, m, stream) : mha_launch<128, false>(p, m, stream);
+}
+
+}  // extern "C"

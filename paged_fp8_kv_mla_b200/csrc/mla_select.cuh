@@ -1,0 +1,211 @@
+// Which keys a request keeps (sm_100a).  Request b holds n_b keys with accumulated weights
+// scores[b][0 .. n_b); when n_b exceeds the budget it keeps its first `num_sink` keys, its last
+// `num_recent` keys and, of those between, the budget - num_sink - num_recent with the largest
+// weights; ties go to the lowest index.  A request within the budget keeps everything.  The kept
+// indices come out ascending.
+//
+// The weights between the two protected ends are mapped to unsigned keys that order like the numbers
+// (-0 as +0, NaN below every number) and the smallest kept key is found by a radix selection over
+// digits of 11, 11 and 10 bits: three histograms, no sort.  A second pass over the keys writes the
+// indices in order, with counts from warp ballots.
+//
+// What bounds it.  4 bytes per key are read once; at these sizes (a few MB at most) that is under a
+// microsecond of HBM time, and the time goes to the chain of passes: load, three histograms, output.
+// So a request is spread over a thread-block cluster: every CTA holds its share of the keys in shared
+// memory (read from HBM once), histograms are added up through distributed shared memory (CTA r adds
+// slice r of the bins of all CTAs and hands the sums to all), and the passes are separated by cluster
+// barriers instead of kernel launches.
+#pragma once
+#include <cstdint>
+#include "mla_kernels.cuh"
+
+namespace mla {
+
+struct SelectParams {
+  const float* scores;             // row stride scores_stride
+  const uint32_t* lengths;         // [B]
+  int32_t* kept;                   // row stride kept_stride
+  int32_t* kept_lengths;           // [B]
+  unsigned int* status;
+  long long scores_stride, kept_stride;
+  unsigned int max_length;
+  int budget, recent, sink;
+};
+
+constexpr int SEL_THREADS = 512;
+constexpr int SEL_WARPS = SEL_THREADS / 32;
+constexpr int SEL_BINS = 2048;
+constexpr int SEL_MAX_CLUSTER = 16;
+constexpr int SEL_CACHE = 40960;   // keys a CTA holds in shared memory; keys past these are read again
+
+// Shared memory: three histograms and the cluster-wide sums, then the keys.
+struct SelectShared {
+  uint32_t hist[3][SEL_BINS];
+  uint32_t total[SEL_BINS];
+  uint32_t counts[SEL_MAX_CLUSTER][2];   // kept and tied keys of each CTA of the cluster
+  uint32_t warp_gt[SEL_WARPS], warp_eq[SEL_WARPS];
+  uint32_t scan[SEL_WARPS];
+  uint32_t bin, need;
+};
+constexpr uint32_t SEL_KEYS_OFF = (sizeof(SelectShared) + 15) / 16 * 16;
+static_assert(SEL_KEYS_OFF + SEL_CACHE * 4 <= 232448, "shared memory map exceeds 227 KB");
+
+__device__ __forceinline__ uint32_t select_key(float x) {
+  if (x != x) return 0u;
+  const uint32_t u = __float_as_uint(x + 0.f);           // -0 + 0 = +0
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(SEL_THREADS, 1) mla_select_kernel(const __grid_constant__ SelectParams p) {
+  extern __shared__ __align__(16) uint8_t sel_smem[];
+  SelectShared& s = *reinterpret_cast<SelectShared*>(sel_smem);
+  uint32_t* cache = reinterpret_cast<uint32_t*>(sel_smem + SEL_KEYS_OFF);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t ncta;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ncta));
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int b = static_cast<int>(ptx::cluster_id_x());
+  const uint32_t given = p.lengths[b];
+  const uint32_t n = min(given, p.max_length);
+  const uint32_t count = min(n, static_cast<uint32_t>(p.budget));
+  int32_t* out = p.kept + b * p.kept_stride;
+  if (rank == 0 && tid == 0) {
+    if (given > p.max_length) raise_status(p.status, STATUS_BOUNDS);
+    p.kept_lengths[b] = static_cast<int32_t>(count);
+  }
+  // the protected ends (and, within the budget, every key)
+  const bool all = n <= static_cast<uint32_t>(p.budget);
+  const uint32_t head = all ? n : p.sink, tail = all ? 0 : p.recent;
+  const uint32_t gtid = rank * SEL_THREADS + tid, gthreads = ncta * SEL_THREADS;
+  for (uint32_t j = gtid; j < head; j += gthreads) out[j] = static_cast<int32_t>(j);
+  for (uint32_t j = gtid; j < tail; j += gthreads) out[count - tail + j] = static_cast<int32_t>(n - tail + j);
+  const uint32_t need0 = count - head - tail;            // keys to choose from the middle
+  if (need0 == 0) return;                                // the same for every CTA of the cluster
+
+  // this CTA's share [lo, hi) of the middle, and each warp's share of that (multiples of 32 keys, so
+  // that indices ascend over lanes, steps, warps and CTAs)
+  const uint32_t mid = n - head - tail;
+  const uint32_t per = (mid + ncta - 1) / ncta;
+  const uint32_t lo = min(rank * per, mid), hi = min(lo + per, mid), m = hi - lo;
+  const float* src = p.scores + b * p.scores_stride + head + lo;
+  for (uint32_t i = tid; i < 3 * SEL_BINS; i += SEL_THREADS) (&s.hist[0][0])[i] = 0;
+  __syncthreads();
+
+  // Each pass counts the keys that agree with the digits found so far by their next digit.
+  constexpr int shift[3] = {21, 10, 0};
+  constexpr uint32_t bins[3] = {2048, 2048, 1024};
+  uint32_t prefix = 0, need = need0;
+#pragma unroll
+  for (int d = 0; d < 3; ++d) {
+    for (uint32_t i0 = 0; i0 < m; i0 += SEL_THREADS) {
+      const uint32_t i = i0 + tid;
+      uint32_t k = 0;
+      bool in = i < m;
+      if (in) {
+        if (d == 0 || i >= SEL_CACHE) k = select_key(src[i]);
+        else k = cache[i];
+        if (d == 0 && i < SEL_CACHE) cache[i] = k;
+        if (d > 0) in = (k >> shift[d > 0 ? d - 1 : 0]) == prefix;
+      }
+      // one addition per warp where all its keys fall into one bin (equal weights, zeros)
+      const uint32_t bin = in ? (k >> shift[d]) & (bins[d] - 1) : bins[d];
+      int same;
+      __match_all_sync(0xffffffffu, bin, &same);
+      if (same) {
+        if (in && lane == 0) atomicAdd(&s.hist[d][bin], 32u);
+      } else if (in) {
+        atomicAdd(&s.hist[d][bin], 1u);
+      }
+    }
+    ptx::cluster_sync();                                 // every CTA's histogram is complete
+    const uint32_t slice = bins[d] / ncta;
+    for (uint32_t i = tid; i < slice; i += SEL_THREADS) {
+      const uint32_t bin = rank * slice + i;
+      uint32_t sum = 0;
+      for (uint32_t q = 0; q < ncta; ++q) sum += ld_cluster_u32(ptx::mapa(ptx::smem_u32(&s.hist[d][bin]), q));
+      for (uint32_t q = 0; q < ncta; ++q) ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&s.total[bin]), q), sum);
+    }
+    ptx::cluster_sync();                                 // every CTA holds the sums
+    // the bin of the need-th largest key: thread t owns bins [t * each, (t + 1) * each) from the top
+    const int each = bins[d] / SEL_THREADS;              // 4 or 2
+    uint32_t own = 0;
+    for (int x = 0; x < each; ++x) own += s.total[bins[d] - 1 - (tid * each + x)];
+    uint32_t inc = own;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 31) s.scan[warp] = inc;
+    __syncthreads();
+    uint32_t above = inc - own;
+    for (int w = 0; w < warp; ++w) above += s.scan[w];
+    for (int x = 0; x < each; ++x) {
+      const uint32_t bin = bins[d] - 1 - (tid * each + x), c = s.total[bin];
+      if (above < need && need <= above + c) {
+        s.bin = bin;
+        s.need = need - above;
+      }
+      above += c;
+    }
+    __syncthreads();
+    prefix = d == 2 ? (prefix << 10) | s.bin : (prefix << 11) | s.bin;
+    need = s.need;                                       // keys still to take among those equal so far
+    // (s.total is written again only after the next pass's first cluster barrier)
+  }
+  const uint32_t cut = prefix;                           // keep keys > cut, and the first `need` equal to it
+
+  const uint32_t wper = ((m + SEL_WARPS - 1) / SEL_WARPS + 31) / 32 * 32;
+  const uint32_t w0 = min(warp * wper, m), w1 = min(w0 + wper, m);
+  uint32_t gt = 0, eq = 0;
+  for (uint32_t i0 = w0; i0 < w1; i0 += 32) {
+    const uint32_t i = i0 + lane;
+    const uint32_t k = i >= w1 ? 0 : i < SEL_CACHE ? cache[i] : select_key(src[i]);
+    gt += __popc(__ballot_sync(0xffffffffu, i < w1 && k > cut));
+    eq += __popc(__ballot_sync(0xffffffffu, i < w1 && k == cut));
+  }
+  if (lane == 0) {
+    s.warp_gt[warp] = gt;
+    s.warp_eq[warp] = eq;
+  }
+  __syncthreads();
+  if (tid < static_cast<int>(ncta)) {
+    uint32_t cg = 0, ce = 0;
+    for (int w = 0; w < SEL_WARPS; ++w) {
+      cg += s.warp_gt[w];
+      ce += s.warp_eq[w];
+    }
+    ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&s.counts[rank][0]), tid), cg);
+    ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&s.counts[rank][1]), tid), ce);
+  }
+  ptx::cluster_sync();                                   // the last access to another CTA's memory
+  uint32_t ties = 0, at = head;                          // ties before this warp, its first output slot
+  for (uint32_t q = 0; q < rank; ++q) {
+    at += s.counts[q][0];
+    ties += s.counts[q][1];
+  }
+  for (int w = 0; w < warp; ++w) {
+    at += s.warp_gt[w];
+    ties += s.warp_eq[w];
+  }
+  at += min(ties, need);
+  const uint32_t below = (1u << lane) - 1;
+  for (uint32_t i0 = w0; i0 < w1; i0 += 32) {
+    const uint32_t i = i0 + lane;
+    const uint32_t k = i >= w1 ? 0 : i < SEL_CACHE ? cache[i] : select_key(src[i]);
+    const bool is_eq = i < w1 && k == cut;
+    const uint32_t e = __ballot_sync(0xffffffffu, is_eq);
+    const bool keep = (i < w1 && k > cut) || (is_eq && ties + __popc(e & below) < need);
+    const uint32_t kb = __ballot_sync(0xffffffffu, keep);
+    if (keep) out[at + __popc(kb & below)] = static_cast<int32_t>(head + lo + i);
+    at += __popc(kb);
+    ties += __popc(e);
+  }
+}
+
+}  // namespace mla
