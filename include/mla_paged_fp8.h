@@ -335,8 +335,8 @@ mla_status_t mla_merge_lse_parts_bf16(const void* outs, const float* lses, int32
  * products are those of the unrounded keys e4m3 * s_t (as in mla_decode_paged_fp8_scale_folded, whose
  * lse makes a row's weights sum to 1 to fp32; with the lse of mla_decode_paged_fp8, which rounds each
  * key element to bf16, a row's sum is off by that rounding, up to a few 1e-3).  q enters exactly: each
- * head's row is split into two e4m3 terms after scaling by a power of two (elements below 2^-10 of the
- * row's largest are off by at most 2^-17 of it).  A (query token, head) whose lse is -inf adds nothing;
+ * head's row is split into two e4m3 terms after scaling by a power of two (elements below 2^-13 of the
+ * row's largest are off by at most 2^-21 of it).  A (query token, head) whose lse is -inf adds nothing;
  * a non-finite q row or lse makes the request's sums NaN, a NaN code only its own key's.  Sums are fp32
  * in a fixed order: results are the same from run to run.
  *
@@ -345,9 +345,12 @@ mla_status_t mla_merge_lse_parts_bf16(const void* outs, const float* lses, int32
  *   lse           fp32 [batch, max_prompt_length, num_q_heads], natural log, read
  *   scores        fp32, row b at scores + b * scores_stride; may be NULL (all zero)
  *   out           fp32, row b at out + b * out_stride; may be scores itself (same stride)
- * Rows hold at least max_cache_length + max_prompt_length values (else MLA_ERR_INVALID_ARG).  No
- * workspace: calls on different streams may overlap, and the call can be captured after one call on
- * the device.  The keys of a page id past the pool are left as they were and flagged
+ *   workspace     device memory of at least mla_accumulate_workspace_bytes bytes, 16-byte aligned, for
+ *                 the split q.  It is the caller's: calls that overlap on the device, or captured graphs
+ *                 that are replayed at the same time, need one each.  Nothing in it has to start at zero
+ *                 and nothing is kept in it from call to call.
+ * Rows hold at least max_cache_length + max_prompt_length values (else MLA_ERR_INVALID_ARG).  The
+ * first call on a device is made outside stream capture.  The keys of a page id past the pool are left as they were and flagged
  * (MLA_ERR_DEVICE_BOUNDS), and a length above max_cache_length is clamped to it and flagged.
  */
 mla_status_t mla_accumulate_weights_fp8(
@@ -355,7 +358,10 @@ mla_status_t mla_accumulate_weights_fp8(
     const uint32_t* cache_lengths, const uint32_t* lookup_table, const uint32_t* scales_lookup_table,
     uint32_t max_prompt_length, uint32_t max_cache_length, uint32_t layer_idx, float softmax_scale,
     const mla_paged_shape_t* shape, const float* scores, int64_t scores_stride,
-    float* out, int64_t out_stride, cudaStream_t stream);
+    float* out, int64_t out_stride, void* workspace, uint64_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace that mla_accumulate_weights_fp8 needs (shape: batch and num_q_heads are read). */
+mla_status_t mla_accumulate_workspace_bytes(uint32_t max_prompt_length, const mla_paged_shape_t* shape, uint64_t* bytes);
 
 /*
  * mla_select_keys -- the keys each request keeps.  Request b holds lengths[b] keys with weights

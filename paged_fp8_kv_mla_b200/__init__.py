@@ -10,4 +10,5 @@ from ._lib import (  # noqa: F401
     release_workspace, version, set_timing_events, load, LIB_PATH, EXPORTED, merge_parts, decode_noalloc,
     decode_host, VARIANT_DECODE, VARIANT_SCALE_FOLDED, VARIANT_E4M3_PV,
     accumulate_weights, select_keys, compact_cache, mha_kv_store, mha_decode, mha_decode_workspace_bytes,
+    accumulate_workspace_bytes,
 )

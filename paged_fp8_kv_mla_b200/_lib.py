@@ -26,7 +26,7 @@ EXPORTED = ["mla_decode_paged_fp8", "mla_gather_dequant_bf16", "mla_set_num_clus
             "mla_release_workspace", "mla_version", "mla_set_timing_events", "mla_decode_paged_fp8_noalloc",
             "mla_kv_store_fp8", "mla_decode_paged_fp8_scale_folded", "mla_merge_lse_parts_bf16",
             "mla_set_wait_limit_ns", "mla_debug_withhold_arrival_once", "mla_decode_paged_fp8_e4m3_pv",
-            "mla_decode_paged_fp8_host", "mla_accumulate_weights_fp8", "mla_select_keys", "mla_compact_paged",
+            "mla_decode_paged_fp8_host", "mla_accumulate_weights_fp8", "mla_accumulate_workspace_bytes", "mla_select_keys", "mla_compact_paged",
             "mla_mha_kv_store", "mla_mha_decode_paged", "mla_mha_decode_workspace_bytes"]
 
 VARIANT_DECODE, VARIANT_SCALE_FOLDED, VARIANT_E4M3_PV = 0, 1, 2
@@ -77,8 +77,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mla_kv_store_fp8.argtypes = [vp, vp, vp, vp, u32, u32, ctypes.POINTER(PagedShape), vp, vp, vp]
     lib.mla_kv_store_fp8.restype = ctypes.c_int
     shp, i64, u64 = ctypes.POINTER(PagedShape), ctypes.c_int64, ctypes.c_uint64
-    lib.mla_accumulate_weights_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, u32, u32, u32, f32, shp, vp, i64, vp, i64, vp]
+    lib.mla_accumulate_weights_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, u32, u32, u32, f32, shp, vp, i64, vp, i64,
+                                               vp, u64, vp]
     lib.mla_accumulate_weights_fp8.restype = ctypes.c_int
+    lib.mla_accumulate_workspace_bytes.argtypes = [u32, shp, ctypes.POINTER(u64)]
+    lib.mla_accumulate_workspace_bytes.restype = ctypes.c_int
     lib.mla_select_keys.argtypes = [vp, i64, vp, i32, u32, i32, i32, i32, vp, i64, vp, vp]
     lib.mla_select_keys.restype = ctypes.c_int
     lib.mla_compact_paged.argtypes = [vp, i64, i32, vp, vp, vp, u32, i32, shp, vp, vp, vp, i64, i32, vp]
@@ -349,64 +352,159 @@ def gather_dequant(blocks, scales, cache_lengths, lookup_table, scales_lookup_ta
     return out_k
 
 
-# ---------------------------------------------------------------- eviction from the latent cache
-def _on(t, stream):
-    """The call's device and stream: the tensors' device whatever the current one, and its current
-    stream unless `stream` is given."""
-    return torch.cuda.device(t.device), _stream(torch.cuda.current_stream(t.device) if stream is None else stream)
+# ---------------------------------------------------------------- cache operators
+# These calls are short, so the binding's own time counts: a tensor that is as expected passes one
+# compound test, and only one that is not goes through _expect, which says what is wrong with it.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _rows(name, t, dtypes, batch, cols):
-    """A [batch, >= cols] tensor whose rows are contiguous (the row stride is free)."""
+def _plain(t, dtype, ndim):
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()
+
+
+def _rows(name, t, dtype, batch, cols):
+    """A [batch, >= cols] tensor whose rows are contiguous (the row stride is free); returns the stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must have dtype {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must have dtype {dtype} (got {t.dtype})")
     if t.dim() != 2 or t.shape[0] != batch or t.shape[1] < cols:
         raise ValueError(f"{name} must be [{batch}, >= {cols}] (got shape {tuple(t.shape)})")
-    if (t.shape[1] > 1 and t.stride(1) != 1) or (batch > 1 and t.stride(0) < t.shape[1]):
+    n = t.shape[1]
+    if batch <= 1:
+        if n > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        return n
+    step, inner = t.stride()
+    if (n > 1 and inner != 1) or step < n:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return step
 
 
-def _row_stride(t):
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+def _one_device(first, *rest):
+    """Index of the one CUDA device that all tensors are on."""
+    d = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != d:
+            d = -1
+    if d < 0:
+        _same_device(first, *rest)
+        raise ValueError("all tensors must be CUDA tensors")
+    return d
+
+
+def _raw_stream(stream, device):
+    """Stream handle: the device's current stream unless `stream` is given."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _run(device, fn, *args):
+    """One library call, on the tensors' device whatever the current one."""
+    if torch.cuda.current_device() == device:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != MLA_OK:
+        _check(st)
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _allocating_on(stream, device):
+    """Allocations for a call belong to the stream that it runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(_raw_stream(stream, device), torch.device("cuda", device)))
+
+
+def _scratch(n, device, stream):
+    if stream is None:
+        return torch.empty(n, dtype=_U8, device=torch.device("cuda", device)) if n else None
+    with _allocating_on(stream, device):
+        return torch.empty(n, dtype=_U8, device=torch.device("cuda", device)) if n else None
+
+
+def _check_tables(cache_lengths, lookup_table, scales_lookup_table, batch):
+    if not (_plain(cache_lengths, _I32, 1) and _plain(lookup_table, _I32, 2)):
+        _expect("cache_lengths", cache_lengths, _U32, ndim=1)
+        _expect("lookup_table", lookup_table, _U32, ndim=2)
+    if cache_lengths.shape[0] != batch or lookup_table.shape[0] != batch:
+        raise ValueError(f"cache_lengths and lookup_table must have {batch} rows (one per request)")
+    _check_scale_table(lookup_table, scales_lookup_table)
+
+
+def _check_scale_table(lookup_table, scales_lookup_table):
+    if scales_lookup_table is not None:
+        _expect("scales_lookup_table", scales_lookup_table, _U32, ndim=2)
+        if scales_lookup_table.shape != lookup_table.shape:
+            raise ValueError("scales_lookup_table must have the shape of lookup_table")
+
+
+def _token_count(max_prompt_length, tokens):
+    if max_prompt_length != tokens:
+        raise ValueError(f"max_prompt_length must be q's number of tokens, {tokens} (got {max_prompt_length})")
 
 
 def accumulate_weights(q, lse, blocks, scales, cache_lengths, lookup_table, scales_lookup_table,
                        max_prompt_length: int, max_cache_length: int, layer_idx: int, softmax_scale: float,
-                       scores=None, out=None, stream=None):
+                       scores=None, out=None, stream=None, workspace=None):
     """mla_accumulate_weights_fp8: add to every cached key the softmax weight it received in this step.
 
     q bf16 [B, T, H, 576] and the cache as for decode(), lse fp32 [B, T, H] as decode() returned it.
     scores fp32 [B, >= max_cache_length + T] (rows may be strided), or None for all zero; entries of the
     step's own tokens start at 0.  Writes out (default: scores itself, or a new tensor) and returns it;
-    entries past a request's keys are left as they were.
+    entries past a request's keys are left as they were.  workspace: a uint8 tensor of
+    accumulate_workspace_bytes(B, T, H) bytes; by default one is taken from torch's allocator for the call.
     """
-    _expect("q", q, (torch.bfloat16,), ndim=4, last=576)
+    if not (_plain(q, _BF16, 4) and _plain(lse, _F32, 3)) or q.shape[3] != 576:
+        _expect("q", q, (_BF16,), ndim=4, last=576)
+        _expect("lse", lse, (_F32,), ndim=3)
     B, T, H, _ = q.shape
-    _expect("lse", lse, (torch.float32,), ndim=3)
-    if tuple(lse.shape) != (B, T, H):
+    if lse.shape != (B, T, H):
         raise ValueError(f"lse must be {(B, T, H)} (got {tuple(lse.shape)})")
-    _check_cache(blocks, scales, cache_lengths, lookup_table, scales_lookup_table, B)
-    if int(max_prompt_length) != T:
-        raise ValueError(f"max_prompt_length must be q's number of tokens, {T} (got {max_prompt_length})")
-    need = int(max_cache_length) + T
-    if scores is not None:
-        _rows("scores", scores, (torch.float32,), B, need)
-    if out is not None:
-        _rows("out", out, (torch.float32,), B, need)
-    _same_device(q, lse, blocks, scales, cache_lengths, lookup_table, scales_lookup_table, scores, out)
+    if not (_plain(blocks, _U8, 6) and _plain(scales, _F32, 6)):
+        _expect("blocks", blocks, _CODES, ndim=6)
+        _expect("scales", scales, (_F32,), ndim=6)
+    _check_tables(cache_lengths, lookup_table, scales_lookup_table, B)
+    _token_count(max_prompt_length, T)
+    shp = paged_shape(B, H, blocks, scales, lookup_table)
+    if scales.shape[1:5] != (shp.kv_dim, shp.num_layers, shp.page_size, shp.num_kv_heads):
+        raise ValueError("scales must match blocks in kv_dim, num_layers, page_size and num_heads")
+    if scales_lookup_table is None and shp.num_scale_blocks != shp.num_blocks:
+        raise ValueError("without a scales_lookup_table, scales must have as many blocks as blocks")
+    need = max_cache_length + T
+    sstep = 0 if scores is None else _rows("scores", scores, _F32, B, need)
+    ostep = 0 if out is None else _rows("out", out, _F32, B, need)
+    _expect("workspace", workspace, (_U8,), ndim=1, optional=True)
+    dev = _one_device(q, lse, blocks, scales, cache_lengths, lookup_table, scales_lookup_table, scores, out, workspace)
     lib = load()
-    dev, st = _on(q, stream)
-    with dev:
-        if out is None:
-            out = torch.zeros((B, need), dtype=torch.float32, device=q.device) if scores is None else scores
-        shp = paged_shape(B, H, blocks, scales, lookup_table)
-        _check(lib.mla_accumulate_weights_fp8(
-            _ptr(q), _ptr(lse), _ptr(blocks), _ptr(scales), _ptr(cache_lengths), _ptr(lookup_table),
-            _ptr(scales_lookup_table), T, int(max_cache_length), int(layer_idx), float(softmax_scale),
-            ctypes.byref(shp), _ptr(scores), 0 if scores is None else _row_stride(scores), _ptr(out), _row_stride(out), st))
+    if out is None:
+        if scores is None:
+            with _allocating_on(stream, dev):
+                out = torch.zeros((B, need), dtype=_F32, device=q.device)
+            ostep = need
+        else:
+            out, ostep = scores, sstep
+    if workspace is None:
+        workspace = _scratch(accumulate_workspace_bytes(B, T, H), dev, stream)
+    _run(dev, lib.mla_accumulate_weights_fp8, q.data_ptr(), lse.data_ptr(), blocks.data_ptr(), scales.data_ptr(),
+         cache_lengths.data_ptr(), lookup_table.data_ptr(), _adr(scales_lookup_table), T, int(max_cache_length), int(layer_idx),
+         float(softmax_scale), ctypes.byref(shp), _adr(scores), sstep, out.data_ptr(), ostep, _adr(workspace),
+         0 if workspace is None else workspace.numel(), _raw_stream(stream, dev))
     return out
+
+
+def accumulate_workspace_bytes(batch: int, max_prompt_length: int, num_q_heads: int) -> int:
+    """Bytes of workspace that accumulate_weights needs."""
+    n, shp = ctypes.c_uint64(0), PagedShape(batch, num_q_heads)
+    _check(load().mla_accumulate_workspace_bytes(max_prompt_length, ctypes.byref(shp), ctypes.byref(n)))
+    return n.value
 
 
 def select_keys(scores, lengths, max_length: int, budget: int, num_recent: int = 0, num_sink: int = 0, kept=None,
@@ -418,24 +516,24 @@ def select_keys(scores, lengths, max_length: int, budget: int, num_recent: int =
     keys with the largest scores between (ties to the lowest index); kept[b, :kept_lengths[b]] ascends
     and later entries are left as they were (0 in a new tensor).
     """
-    _expect("lengths", lengths, _U32, ndim=1)
+    if not _plain(lengths, _I32, 1):
+        _expect("lengths", lengths, _U32, ndim=1)
     B = lengths.shape[0]
-    _rows("scores", scores, (torch.float32,), B, int(max_length))
-    if kept is not None:
-        _rows("kept", kept, (torch.int32,), B, min(int(budget), int(max_length)))
-    _expect("kept_lengths", kept_lengths, (torch.int32,), ndim=1, optional=True)
-    if kept_lengths is not None and kept_lengths.shape[0] != B:
-        raise ValueError(f"kept_lengths must have {B} entries")
-    _same_device(scores, lengths, kept, kept_lengths)
+    sstep = _rows("scores", scores, _F32, B, max_length)
+    kstep = 0 if kept is None else _rows("kept", kept, _I32, B, min(budget, max_length))
+    if kept_lengths is not None and (not _plain(kept_lengths, _I32, 1) or kept_lengths.shape[0] != B):
+        raise ValueError(f"kept_lengths must be a contiguous int32 tensor of {B} entries")
+    dev = _one_device(scores, lengths, kept, kept_lengths)
     lib = load()
-    dev, st = _on(scores, stream)
-    with dev:
-        if kept is None:
-            kept = torch.zeros((B, max(int(budget), 1)), dtype=torch.int32, device=scores.device)
-        if kept_lengths is None:
-            kept_lengths = torch.empty(B, dtype=torch.int32, device=scores.device)
-        _check(lib.mla_select_keys(_ptr(scores), _row_stride(scores), _ptr(lengths), B, int(max_length), int(budget),
-                                   int(num_recent), int(num_sink), _ptr(kept), _row_stride(kept), _ptr(kept_lengths), st))
+    if kept is None or kept_lengths is None:
+        with _allocating_on(stream, dev):
+            if kept is None:
+                kstep = max(budget, 1)
+                kept = torch.zeros((B, kstep), dtype=_I32, device=scores.device)
+            if kept_lengths is None:
+                kept_lengths = torch.empty(B, dtype=_I32, device=scores.device)
+    _run(dev, lib.mla_select_keys, scores.data_ptr(), sstep, lengths.data_ptr(), B, int(max_length), int(budget),
+         int(num_recent), int(num_sink), kept.data_ptr(), kstep, kept_lengths.data_ptr(), _raw_stream(stream, dev))
     return kept, kept_lengths
 
 
@@ -446,82 +544,74 @@ def compact_cache(kept, kept_lengths, lookup_table, scales_lookup_table, layer_i
 
     kept int32 [B, n] and kept_lengths int32 [B] as select_keys() returns them (strictly ascending).
     Returns (blocks, scales, scores)."""
-    _expect("blocks", blocks, _CODES + (torch.bfloat16,), ndim=6)
-    _expect("scales", scales, (torch.float32,), ndim=6, optional=True)
-    _expect("kept_lengths", kept_lengths, (torch.int32,), ndim=1)
+    if not _plain(blocks, _U8, 6):
+        _expect("blocks", blocks, _CODES + (_BF16,), ndim=6)
+    _expect("scales", scales, (_F32,), ndim=6, optional=True)
+    if not (_plain(kept_lengths, _I32, 1) and _plain(lookup_table, _I32, 2)):
+        _expect("kept_lengths", kept_lengths, (_I32,), ndim=1)
+        _expect("lookup_table", lookup_table, _U32, ndim=2)
     B = kept_lengths.shape[0]
-    _rows("kept", kept, (torch.int32,), B, 1)
-    _expect("lookup_table", lookup_table, _U32, ndim=2)
-    _expect("scales_lookup_table", scales_lookup_table, _U32, ndim=2, optional=True)
     if lookup_table.shape[0] != B:
         raise ValueError(f"lookup_table must have {B} rows (one per request)")
-    if scales_lookup_table is not None and tuple(scales_lookup_table.shape) != tuple(lookup_table.shape):
-        raise ValueError("scales_lookup_table must have the shape of lookup_table")
-    if scales is not None and tuple(scales.shape[1:5]) != tuple(blocks.shape[1:5]):
-        raise ValueError("scales must match blocks in kv_dim, num_layers, page_size and num_heads")
-    if scales is not None and scales_lookup_table is None and scales.shape[0] != blocks.shape[0]:
-        raise ValueError("without a scales_lookup_table, scales must have as many blocks as blocks")
-    if scores is not None:
-        _rows("scores", scores, (torch.float32,), B, 1)
-    _same_device(kept, kept_lengths, lookup_table, scales_lookup_table, blocks, scales, scores)
-    lib = load()
+    _check_scale_table(lookup_table, scales_lookup_table)
+    kstep = _rows("kept", kept, _I32, B, 1)
     NB, KVD, NL, P, NKV, D = blocks.shape
-    shp = PagedShape(batch=B, num_q_heads=0, head_dim=D, v_dim=0, num_blocks=NB, kv_dim=KVD, num_layers=NL, page_size=P,
-                     num_kv_heads=NKV, num_scale_blocks=NB if scales is None else scales.shape[0],
-                     head_dim_granularity=1 if scales is None else scales.shape[-1], max_pages=lookup_table.shape[1])
-    dev, st = _on(blocks, stream)
-    with dev:
-        _check(lib.mla_compact_paged(
-            _ptr(kept), _row_stride(kept), kept.shape[1], _ptr(kept_lengths), _ptr(lookup_table), _ptr(scales_lookup_table),
-            int(layer_idx), blocks.element_size(), ctypes.byref(shp), _ptr(blocks), _ptr(scales), _ptr(scores),
-            0 if scores is None else _row_stride(scores), 0 if scores is None else scores.shape[1], st))
+    NSB, g = NB, 1
+    if scales is not None:
+        NSB, g = scales.shape[0], scales.shape[5]
+        if scales.shape[1:5] != (KVD, NL, P, NKV):
+            raise ValueError("scales must match blocks in kv_dim, num_layers, page_size and num_heads")
+        if scales_lookup_table is None and NSB != NB:
+            raise ValueError("without a scales_lookup_table, scales must have as many blocks as blocks")
+    sstep = 0 if scores is None else _rows("scores", scores, _F32, B, 1)
+    dev = _one_device(kept, kept_lengths, lookup_table, scales_lookup_table, blocks, scales, scores)
+    shp = PagedShape(B, 0, D, 0, NB, KVD, NL, P, NKV, NSB, g, lookup_table.shape[1])
+    _run(dev, load().mla_compact_paged, kept.data_ptr(), kstep, kept.shape[1], kept_lengths.data_ptr(),
+         lookup_table.data_ptr(), _adr(scales_lookup_table), int(layer_idx), blocks.element_size(), ctypes.byref(shp),
+         blocks.data_ptr(), _adr(scales), _adr(scores), sstep, 0 if scores is None else scores.shape[1],
+         _raw_stream(stream, dev))
     return blocks, scales, scores
 
 
-# ---------------------------------------------------------------- multi-head cache
-def _check_mha(blocks, scales, cache_lengths, lookup_table, scales_lookup_table, batch, kv_heads, dim):
-    """The 6-D multi-head cache (keys in kv plane 0, values in plane 1); returns its shape record but for
-    num_q_heads, which the caller fills in."""
-    _expect("blocks", blocks, _CODES + (torch.bfloat16,), ndim=6)
-    fp8 = blocks.dtype != torch.bfloat16
-    _expect("scales", scales, (torch.float32,), ndim=6, optional=not fp8)
-    if scales is not None and not fp8:
-        raise ValueError("a bf16 cache takes no scales")
-    _expect("cache_lengths", cache_lengths, _U32, ndim=1)
-    _expect("lookup_table", lookup_table, _U32, ndim=2)
-    _expect("scales_lookup_table", scales_lookup_table, _U32, ndim=2, optional=True)
+def _check_mha(blocks, scales, cache_lengths, lookup_table, scales_lookup_table, batch, heads, kv_heads, dim):
+    """Shape record of the 6-D multi-head cache (keys in kv plane 0, values in plane 1)."""
+    bf16 = _plain(blocks, _BF16, 6)
+    if not bf16 and not _plain(blocks, _U8, 6):
+        _expect("blocks", blocks, _CODES + (_BF16,), ndim=6)
     NB, KVD, NL, P, NKV, D = blocks.shape
-    if (NKV, D) != (kv_heads, dim):
-        raise ValueError(f"blocks hold {NKV} heads of {D} values, expected {kv_heads} of {dim}")
-    if fp8 and (tuple(scales.shape[1:5]) != (KVD, NL, P, NKV) or scales.shape[5] != 1):
-        raise ValueError(f"scales must be [n, {KVD}, {NL}, {P}, {NKV}, 1] (got {tuple(scales.shape)})")
-    if fp8 and scales_lookup_table is None and scales.shape[0] != NB:
-        raise ValueError("without a scales_lookup_table, scales must have as many blocks as blocks")
-    if cache_lengths.shape[0] != batch or lookup_table.shape[0] != batch:
-        raise ValueError(f"cache_lengths and lookup_table must have {batch} rows (one per request)")
-    if scales_lookup_table is not None and tuple(scales_lookup_table.shape) != tuple(lookup_table.shape):
-        raise ValueError("scales_lookup_table must have the shape of lookup_table")
-    return PagedShape(batch=batch, num_q_heads=0, head_dim=D, v_dim=D, num_blocks=NB, kv_dim=KVD, num_layers=NL,
-                      page_size=P, num_kv_heads=NKV, num_scale_blocks=scales.shape[0] if fp8 else NB,
-                      head_dim_granularity=1, max_pages=lookup_table.shape[1])
+    if D != dim or (kv_heads and NKV != kv_heads):
+        raise ValueError(f"blocks hold {NKV} heads of {D} values, expected {kv_heads or NKV} of {dim}")
+    NSB = NB
+    if bf16:
+        if scales is not None:
+            raise ValueError("a bf16 cache takes no scales")
+    else:
+        if not _plain(scales, _F32, 6):
+            _expect("scales", scales, (_F32,), ndim=6)
+        if scales.shape[1:] != (KVD, NL, P, NKV, 1):
+            raise ValueError(f"scales must be [n, {KVD}, {NL}, {P}, {NKV}, 1] (got {tuple(scales.shape)})")
+        NSB = scales.shape[0]
+        if scales_lookup_table is None and NSB != NB:
+            raise ValueError("without a scales_lookup_table, scales must have as many blocks as blocks")
+    _check_tables(cache_lengths, lookup_table, scales_lookup_table, batch)
+    return PagedShape(batch, heads, D, D, NB, KVD, NL, P, NKV, NSB, 1, lookup_table.shape[1])
 
 
 def mha_kv_store(k, v, cache_lengths, lookup_table, scales_lookup_table, layer_idx: int, blocks, scales=None, stream=None):
     """mla_mha_kv_store: write the step's keys and values, bf16 [B, T, HKV, D] each, in place into blocks
     (bf16, or uint8 / e4m3 with scales fp32 [.., HKV, 1]) [NB, kv_dim, L, P, HKV, D] at positions
     cache_lengths[b] + i."""
-    _expect("k", k, (torch.bfloat16,), ndim=4)
-    _expect("v", v, (torch.bfloat16,), ndim=4)
-    if k.shape != v.shape:
-        raise ValueError("k and v must have the same shape")
+    if not (_plain(k, _BF16, 4) and _plain(v, _BF16, 4)):
+        _expect("k", k, (_BF16,), ndim=4)
+        _expect("v", v, (_BF16,), ndim=4)
     B, T, HKV, D = k.shape
-    shp = _check_mha(blocks, scales, cache_lengths, lookup_table, scales_lookup_table, B, HKV, D)
-    _same_device(k, v, blocks, scales, cache_lengths, lookup_table, scales_lookup_table)
-    lib = load()
-    dev, st = _on(k, stream)
-    with dev:
-        _check(lib.mla_mha_kv_store(_ptr(k), _ptr(v), _ptr(cache_lengths), _ptr(lookup_table), _ptr(scales_lookup_table), T,
-                                    int(layer_idx), blocks.element_size(), ctypes.byref(shp), _ptr(blocks), _ptr(scales), st))
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    shp = _check_mha(blocks, scales, cache_lengths, lookup_table, scales_lookup_table, B, 0, HKV, D)
+    dev = _one_device(k, v, blocks, scales, cache_lengths, lookup_table, scales_lookup_table)
+    _run(dev, load().mla_mha_kv_store, k.data_ptr(), v.data_ptr(), cache_lengths.data_ptr(), lookup_table.data_ptr(),
+         _adr(scales_lookup_table), T, int(layer_idx), blocks.element_size(), ctypes.byref(shp), blocks.data_ptr(), _adr(scales),
+         _raw_stream(stream, dev))
     return blocks, scales
 
 
@@ -535,56 +625,44 @@ def mha_decode(q, blocks, scales, cache_lengths, lookup_table, scales_lookup_tab
     mha_decode_workspace_bytes(...) bytes; by default one is taken from torch's allocator for the call.
     Returns (out bf16 [B, T, H, D], lse fp32 [B, T, H] or None).
     """
-    _expect("q", q, (torch.bfloat16,), ndim=4)
+    if not _plain(q, _BF16, 4):
+        _expect("q", q, (_BF16,), ndim=4)
     B, T, H, D = q.shape
-    if int(max_prompt_length) != T:
-        raise ValueError(f"max_prompt_length must be q's number of tokens, {T} (got {max_prompt_length})")
-    if not isinstance(blocks, torch.Tensor) or blocks.dim() != 6:
-        raise ValueError("blocks must be 6-D")
-    shp = _check_mha(blocks, scales, cache_lengths, lookup_table, scales_lookup_table, B, blocks.shape[4], D)
-    shp.num_q_heads = H
-    _expect("out", out, (torch.bfloat16,), ndim=4, optional=True)
-    _expect("lse", lse, (torch.float32,), ndim=3, optional=True)
-    _expect("workspace", workspace, (torch.uint8,), ndim=1, optional=True)
-    if out is not None and out.shape != q.shape:
-        raise ValueError(f"out must be {tuple(q.shape)} (got {tuple(out.shape)})")
-    if lse is not None and tuple(lse.shape) != (B, T, H):
-        raise ValueError(f"lse must be {(B, T, H)} (got {tuple(lse.shape)})")
-    _same_device(q, blocks, scales, cache_lengths, lookup_table, scales_lookup_table, out, lse, workspace)
+    _token_count(max_prompt_length, T)
+    shp = _check_mha(blocks, scales, cache_lengths, lookup_table, scales_lookup_table, B, H, 0, D)
+    if out is not None and (not _plain(out, _BF16, 4) or out.shape != q.shape):
+        raise ValueError(f"out must be a contiguous bf16 tensor of shape {tuple(q.shape)}")
+    if lse is not None and (not _plain(lse, _F32, 3) or lse.shape != (B, T, H)):
+        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(B, T, H)}")
+    _expect("workspace", workspace, (_U8,), ndim=1, optional=True)
+    dev = _one_device(q, blocks, scales, cache_lengths, lookup_table, scales_lookup_table, out, lse, workspace)
     lib = load()
-    dev, st = _on(q, stream)
-    with dev:
-        # what the call allocates belongs to the stream that it runs on
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(
-                stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(st.value or 0, q.device)):
+    if out is None or (lse is None and want_lse):
+        with _allocating_on(stream, dev):
             if out is None:
                 out = torch.empty_like(q)
             if lse is None and want_lse:
-                lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
-            if workspace is None:
-                n = _workspace_bytes(lib, T, max_cache_length, blocks, shp)
-                workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
-        _check(lib.mla_mha_decode_paged(
-            _ptr(q), _ptr(blocks), _ptr(scales), _ptr(cache_lengths), _ptr(lookup_table), _ptr(scales_lookup_table), T,
-            int(max_cache_length), int(layer_idx), float(softmax_scale), blocks.element_size(), ctypes.byref(shp),
-            _ptr(out), _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel(), st))
+                lse = torch.empty((B, T, H), dtype=_F32, device=q.device)
+    if workspace is None:
+        n = ctypes.c_uint64(0)
+        _run(dev, lib.mla_mha_decode_workspace_bytes, T, int(max_cache_length), blocks.element_size(), ctypes.byref(shp),
+             ctypes.byref(n))
+        workspace = _scratch(n.value, dev, stream)
+    _run(dev, lib.mla_mha_decode_paged, q.data_ptr(), blocks.data_ptr(), _adr(scales), cache_lengths.data_ptr(),
+         lookup_table.data_ptr(), _adr(scales_lookup_table), T, int(max_cache_length), int(layer_idx), float(softmax_scale),
+         blocks.element_size(), ctypes.byref(shp), out.data_ptr(), _adr(lse), _adr(workspace),
+         0 if workspace is None else workspace.numel(), _raw_stream(stream, dev))
     return out, lse
-
-
-def _workspace_bytes(lib, T, max_cache_length, blocks, shp):
-    n = ctypes.c_uint64(0)
-    _check(lib.mla_mha_decode_workspace_bytes(int(T), int(max_cache_length), blocks.element_size(), ctypes.byref(shp),
-                                              ctypes.byref(n)))
-    return n.value
 
 
 def mha_decode_workspace_bytes(q, blocks, lookup_table, max_cache_length: int) -> int:
     """Bytes of workspace that mha_decode needs for these tensors (0 for short caches)."""
     NB, KVD, NL, P, NKV, D = blocks.shape
-    shp = PagedShape(batch=q.shape[0], num_q_heads=q.shape[2], head_dim=D, v_dim=D, num_blocks=NB, kv_dim=KVD, num_layers=NL,
-                     page_size=P, num_kv_heads=NKV, num_scale_blocks=NB, head_dim_granularity=1, max_pages=lookup_table.shape[1])
-    with torch.cuda.device(q.device):
-        return _workspace_bytes(load(), q.shape[1], max_cache_length, blocks, shp)
+    shp = PagedShape(q.shape[0], q.shape[2], D, D, NB, KVD, NL, P, NKV, NB, 1, lookup_table.shape[1])
+    n = ctypes.c_uint64(0)
+    _run(q.get_device(), load().mla_mha_decode_workspace_bytes, q.shape[1], int(max_cache_length), blocks.element_size(),
+         ctypes.byref(shp), ctypes.byref(n))
+    return n.value
 
 
 def set_num_clusters(n: int):

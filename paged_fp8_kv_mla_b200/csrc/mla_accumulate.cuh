@@ -10,11 +10,13 @@
 // No conversion of the cache.  The keys go from HBM to the tensor core as the e4m3 bytes they are
 // (kind::f8f6f4) and it is q that is brought to e4m3, without loss: a bf16 value has 8 significant
 // bits and an e4m3 value 4, so after scaling a head's row by a power of two (largest value into
-// [128, 256)) x = hi + lo with hi = e4m3_rn(x) and lo = x - hi, an integer multiple m 2^(e-7) with
-// |m| <= 8, which e4m3 holds exactly while 2^e >= 2^-2.  Smaller elements are off by at most 2^-10,
-// i.e. 2^-17 of the row's largest element.  8-bit MMAs run at twice the 16-bit rate, so the two terms
-// cost what one bf16 product would, and no thread touches the keys.  (The accumulation of
-// kind::f8f6f4 was measured to be that of fp32 sums: 4e-8 relative on K = 576.)
+// [128, 256)) x = hi + lo / 16 with hi = e4m3_rn(x) and lo = 16 (x - hi).  x - hi is m 2^(e-7) with an
+// integer |m| <= 8, which e4m3 holds exactly down to 2^e = 2^-6, i.e. 2^-13 of the row's largest
+// element; smaller elements are off by at most 2^-14, 2^-21 of it.  8-bit MMAs run at twice the 16-bit
+// rate, so the two terms cost what one bf16 product would, and no thread touches the keys.  (The
+// accumulation of kind::f8f6f4 was measured to be that of fp32 sums: 4e-8 relative on K = 576.)
+// The split is a kernel of its own, once per (request, token, head): inside the main kernel every CTA
+// that meets a request would repeat it (measured: 10 us per request and CTA, 20 of 183 us at 128 x 8k).
 //
 // A = K, B = Q.  D has one key per tensor-memory lane and one head per column, so the sum over heads
 // is a sum over a thread's own registers; the per-key factors (scale, mask, running sum) are thread
@@ -28,9 +30,9 @@
 // sums are formed in a fixed order by one thread: no atomics, and the result does not depend on the
 // launch.  K moves through a ring of ten 8 KB slots, one 64-dim column of a tile each, filled by TMA
 // (one box per page run) and released by tcgen05.commit, so loads, MMAs and the exponentials of the
-// tile before overlap.
+// tile before overlap.  q is replaced column by column as the last MMAs of an item release it.
 //
-// Warps: 0 producer, 1 MMA issuer and TMEM owner, 4-7 epilogue (lane quadrants 0-3), 8-15 q split.
+// Warps: 0 K producer, 1 MMA issuer and TMEM owner, 2 q producer, 4-7 epilogue (lane quadrants 0-3).
 #pragma once
 #include <cstdint>
 #include "mla_kernels.cuh"
@@ -41,6 +43,7 @@ struct AccumulateParams {
   CUtensorMap tmap_k;              // blocks as {64 bytes, rows, 9 columns}, box = box_rows rows of a column
   const uint16_t* q;               // bf16 bits [B, T, H, 576]
   const float* lse;                // [B, T, H], natural log
+  uint8_t* split;                  // workspace: per item, q's columns as the MMA reads them, then head factors
   const float* scales;             // [NSB, KVD, NL, P, 1, 1]
   const uint32_t* cache_lengths;   // [B]
   const uint32_t* lut;             // [B, max_pages]
@@ -50,7 +53,9 @@ struct AccumulateParams {
   long long scores_stride, out_stride;
   unsigned int* status;
   unsigned long long wait_limit_ns;
+  uint32_t item_bytes;             // of `split`
   int B, T, H, G, P, KVD, NL, layer, NB, NSB, max_pages, box_rows;
+  int i0, ni;                      // the query tokens of this launch
   unsigned int max_cache_length;
   FastDiv divP, divG;
   float softmax_scale;
@@ -59,33 +64,33 @@ struct AccumulateParams {
 constexpr int ACC_BN = 128;                       // keys per tile (MMA M)
 constexpr int ACC_HEADS = 128;                    // heads per item (MMA N = 2 x heads)
 constexpr int ACC_COLS = HEAD_DIM / 64;           // 9 columns of 64 dims
-constexpr int ACC_THREADS = 512;
+constexpr int ACC_THREADS = 256;
+constexpr int ACC_Q_WARP = 2;
 constexpr int ACC_EPI_WARP0 = 4;
-constexpr int ACC_Q_WARP0 = 8;
-constexpr int ACC_Q_WARPS = 8;
 constexpr int ACC_SLOTS = 10;
 constexpr uint32_t ACC_SLOT_BYTES = ACC_BN * 64;
 constexpr uint32_t ACC_SQ = 0;                    // [9 columns][2 x heads rows (hi, then lo)][64 B]
 constexpr uint32_t ACC_SK = ACC_COLS * 2 * ACC_HEADS * 64;
-constexpr uint32_t ACC_SH = ACC_SK + ACC_SLOTS * ACC_SLOT_BYTES;   // [128] {factor, -lse log2 e}
-constexpr uint32_t ACC_SBAR = ACC_SH + ACC_HEADS * 8;
-constexpr uint32_t ACC_SMISC = ACC_SBAR + 256;
-constexpr uint32_t ACC_SMEM = ACC_SMISC + 64;
-constexpr uint32_t ACC_SMEM_ALLOC = ACC_SMEM + 1024;
-static_assert(ACC_SMEM_ALLOC <= 232448, "shared memory map exceeds 227 KB");
+constexpr uint32_t ACC_SH = ACC_SK + ACC_SLOTS * ACC_SLOT_BYTES;   // [2][128] {factor, -lse log2 e}
+constexpr uint32_t ACC_SBAR = ACC_SH + 2 * ACC_HEADS * 8;
+constexpr uint32_t ACC_SMISC = ACC_SBAR + 512;
+constexpr uint32_t ACC_SMEM = ACC_SMISC + 256;
+constexpr uint32_t ACC_SMEM_ALLOC = 232448;
+static_assert(ACC_SMEM + 255 <= ACC_SMEM_ALLOC, "shared memory map exceeds 227 KB");
 
 enum AccBar : uint32_t {
   AB_K_FULL = 0,                    // [10] producer's expect_tx arrival + the column's bytes
   AB_K_EMPTY = ACC_SLOTS,           // [10] commit: the column's MMAs have read it
   AB_ACC_FULL = 2 * ACC_SLOTS,      // [2] commit: a tile's products are in tensor memory
   AB_ACC_EMPTY = AB_ACC_FULL + 2,   // [2] 128 epilogue threads have read them
-  AB_Q_FULL = AB_ACC_EMPTY + 2,     // 256 q threads: an item's q and head factors are written
-  AB_Q_EMPTY = AB_Q_FULL + 1,       // commit: an item's last MMA is done
-  AB_ITEM_DONE = AB_Q_EMPTY + 1,    // 128 epilogue threads: the item's head factors have been read
-  AB_DRAIN = AB_ITEM_DONE + 1,      // commit at exit
+  AB_Q_FULL = AB_ACC_EMPTY + 2,     // [9] a column of an item's q is in (bytes)
+  AB_Q_EMPTY = AB_Q_FULL + ACC_COLS,   // [9] commit: the item's last MMAs on the column are done
+  AB_H_FULL = AB_Q_EMPTY + ACC_COLS,   // [2] an item's head factors are in (bytes)
+  AB_H_EMPTY = AB_H_FULL + 2,       // [2] 128 epilogue threads have read them
+  AB_DRAIN = AB_H_EMPTY + 2,        // commit at exit
   ACC_BARS
 };
-static_assert(8 * ACC_BARS <= 256, "barrier block overlaps what follows");
+static_assert(8 * ACC_BARS <= 512, "barrier block overlaps what follows");
 
 // D[tmem] (+)= A B^T with e4m3 operands in shared memory (one CTA).
 __device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -95,6 +100,28 @@ __device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
       :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Bounded wait on an mbarrier phase that polls without sleeping: for roles whose every wait sits on the
+// path of a tile (a thread suspended in try_wait resumes hundreds of cycles late).  Looks at the clock
+// and at the abort flag every 256 polls only.
+__device__ __forceinline__ bool spin_bar(uint32_t addr, uint32_t parity, volatile uint32_t* abort, unsigned int* status,
+                                         uint64_t limit) {
+  if (ptx::mbar_test_wait(addr, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  for (uint32_t n = 1;; ++n) {
+    if (ptx::mbar_test_wait(addr, parity)) return true;
+    if ((n & 255u) == 0) {
+      if (*abort) return false;
+      if (ptx::globaltimer() - t0 > limit) return wait_gave_up(abort, status, 0);
+    }
+  }
 }
 
 // 32 lanes x 8 consecutive 32-bit columns.
@@ -141,7 +168,7 @@ struct AccWalker {
   }
   __device__ __forceinline__ bool next_item(const AccumulateParams& p) {
     j = ta;
-    if (++item < p.T * p.G) return true;
+    if (++item < p.ni * p.G) return true;
     if (left <= 0) return false;
     ++b;
     return open(p, 0);
@@ -170,7 +197,7 @@ __device__ __forceinline__ AccKey acc_key(const AccumulateParams& p, int b, int 
   }
   k.scale = p.scales[((static_cast<size_t>(sblk) * p.KVD) * p.NL + p.layer) * p.P + slot];
   k.dst = p.out + b * p.out_stride + t;
-  if (item == 0 && p.scores && t < L) k.base = p.scores[b * p.scores_stride + t];
+  if (item == 0 && p.i0 == 0 && p.scores && t < L) k.base = p.scores[b * p.scores_stride + t];
   return k;
 }
 
@@ -181,84 +208,82 @@ __device__ __forceinline__ void acc_heads(const uint32_t (&hi)[W], const uint32_
 #pragma unroll
   for (int x = 0; x < W; x += 2) {
     const uint4 f = ptx::ld_shared_v4(hf + x * 8);       // {factor, -lse} of two heads
-    const float x0 = (__uint_as_float(hi[x]) + __uint_as_float(lo[x])) * s;
-    const float x1 = (__uint_as_float(hi[x + 1]) + __uint_as_float(lo[x + 1])) * s;
+    const float x0 = fmaf(__uint_as_float(lo[x]), 0.0625f, __uint_as_float(hi[x])) * s;
+    const float x1 = fmaf(__uint_as_float(lo[x + 1]), 0.0625f, __uint_as_float(hi[x + 1])) * s;
     sum[x & 2] += ptx::ex2_approx(fmaf(x0, __uint_as_float(f.x), __uint_as_float(f.y)));
     sum[(x & 2) + 1] += ptx::ex2_approx(fmaf(x1, __uint_as_float(f.z), __uint_as_float(f.w)));
   }
 }
 
-// One 16-byte chunk (8 bf16 values, scaled by m1 * m2, a power of two) as 8 hi and 8 lo codes.
-__device__ __forceinline__ void acc_split8(uint4 v, float m1, float m2, uint2& hi, uint2& lo) {
-  const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-  uint32_t h[4], l[4];
+// ------------------------------------------------------------------ q split
+// Workspace of an item ((b * ni + i) * G + g): 9 columns of 2 hpad rows (hi of each head, then lo) of
+// 64 bytes in the 64-byte swizzle, then {factor, -lse log2 e} of each head; hpad heads, a multiple of 8.
+__device__ __forceinline__ uint32_t acc_hpad(const AccumulateParams& p, int g) {
+  return (min(p.H - g * ACC_HEADS, ACC_HEADS) + 7) & ~7;
+}
+
+// One warp per head row.
+__global__ void __launch_bounds__(256) mla_split_q_kernel(const __grid_constant__ AccumulateParams p) {
+  ptx::griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const uint32_t per_item = (min(p.H, ACC_HEADS) + 7) & ~7;   // rows of an item's workspace
+  const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const long long item = w / per_item;
+  const uint32_t r = static_cast<uint32_t>(w - item * per_item);
+  if (item >= static_cast<long long>(p.B) * p.ni * p.G) return;
+  const long long bi = item / p.G;
+  const int g = static_cast<int>(item - bi * p.G);
+  const uint32_t hpad = acc_hpad(p, g);
+  if (r >= hpad) return;
+  const int b = static_cast<int>(bi / p.ni), i = p.i0 + static_cast<int>(bi - static_cast<long long>(b) * p.ni);
+  const int h = g * ACC_HEADS + r;
+  const bool have = h < p.H;
+  const size_t row = (static_cast<size_t>(b) * p.T + i) * p.H + h;
+  const uint4* src = reinterpret_cast<const uint4*>(p.q + row * HEAD_DIM);
+  const float lse = have ? p.lse[row] : -INFINITY;
+  uint4 v[3];
+  uint32_t m2 = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float a = __uint_as_float(in[k] << 16) * m1 * m2, b = __uint_as_float(in[k] & 0xFFFF0000u) * m1 * m2;
-    h[k] = ptx::e4m3x2_rn_satfinite(a, b);
-    const uint32_t back = ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(h[k]));
-    l[k] = ptx::e4m3x2_rn_satfinite(a - ptx::f16_lo_to_f32(back), b - ptx::f16_hi_to_f32(back));
+  for (int c = 0; c < 3; ++c) {
+    v[c] = have && lane + 32 * c < HEAD_DIM / 8 ? src[lane + 32 * c] : make_uint4(0, 0, 0, 0);
+    m2 = __vmaxu2(__vmaxu2(m2, v[c].x & 0x7FFF7FFFu), v[c].y & 0x7FFF7FFFu);
+    m2 = __vmaxu2(__vmaxu2(m2, v[c].z & 0x7FFF7FFFu), v[c].w & 0x7FFF7FFFu);
   }
-  hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-  lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
-}
-
-__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint2 v) {
-  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(addr), "r"(v.x), "r"(v.y) : "memory");
-}
-
-// Writes one item's q (hi and lo rows, 64-byte swizzled columns) and head factors.  Each warp takes
-// every eighth head row, four rows at a time so that their loads overlap.
-__device__ __forceinline__ void acc_write_q(const AccumulateParams& p, const AccWalker& w, uint32_t base, int wq, int lane,
-                                            int heads, int hpad, uint4 (&v)[4][3], int r0) {
-  const uint32_t col_bytes = static_cast<uint32_t>(hpad) * 128u;
+  const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+  // 2^k with k = 7 - e, e the exponent of the row's largest element (tiny rows: at most 2^126, whose
+  // reciprocal is normal)
+  const int k = m == 0 ? 0 : min(max(7 - (static_cast<int>(m >> 7) - 127), -120), 126);
+  const float f = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+  uint8_t* dst = p.split + item * p.item_bytes;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int r = r0 + u * ACC_Q_WARPS;
-    if (r >= hpad) break;
-    uint32_t m2 = 0;
+  for (int c = 0; c < 3; ++c) {
+    const uint32_t ch = lane + 32 * c;                   // dims 8 ch .. 8 ch + 7
+    if (ch >= HEAD_DIM / 8) break;
+    const uint32_t in[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int c = 0; c < 3; ++c) {
-      m2 = __vmaxu2(m2, v[u][c].x & 0x7FFF7FFFu);
-      m2 = __vmaxu2(m2, v[u][c].y & 0x7FFF7FFFu);
-      m2 = __vmaxu2(m2, v[u][c].z & 0x7FFF7FFFu);
-      m2 = __vmaxu2(m2, v[u][c].w & 0x7FFF7FFFu);
+    for (int x = 0; x < 4; ++x) {
+      // f16 holds the scaled values exactly down to 2^-17 (their 8 bits), far below what lo resolves
+      const uint32_t y = ptx::pack_f16x2(__uint_as_float(in[x] << 16) * f, __uint_as_float(in[x] & 0xFFFF0000u) * f);
+      hi[x] = ptx::e4m3x2_rn_satfinite_f16x2(y);
+      const uint32_t rest = ptx::sub_f16x2(y, ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(hi[x])));
+      lo[x] = ptx::e4m3x2_rn_satfinite_f16x2(mul_f16x2(rest, 0x4C004C00u));   // x 16
     }
-    uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-    m = __reduce_max_sync(0xffffffffu, m);
-    // the row's power of two, 2^(7 - e) with e the exponent of its largest element; as a product of
-    // two factors, since it can be 2^126 (tiny rows: the clamp keeps its reciprocal normal)
-    const int e = static_cast<int>(m >> 7) - 127;
-    const int k = m == 0 ? 0 : min(max(7 - e, -120), 126);
-    const float f1 = __uint_as_float(static_cast<uint32_t>(127 + (k >> 1)) << 23);
-    const float f2 = __uint_as_float(static_cast<uint32_t>(127 + (k - (k >> 1))) << 23);
-#pragma unroll
-    for (int c = 0; c < 3; ++c) {
-      const int ch = lane + 32 * c;
-      if (ch >= HEAD_DIM / 8) break;
-      uint2 hi, lo;
-      acc_split8(v[u][c], f1, f2, hi, lo);
-      const uint32_t a = base + ACC_SQ + (ch >> 3) * col_bytes + (ch & 1) * 8;
-      const uint32_t unit = static_cast<uint32_t>(ch & 7) >> 1;
-      // hpad is a multiple of 8, so the lo row hpad + r has the same swizzle phase as row r
-      const uint32_t off = r * 64u + ((unit ^ ((static_cast<uint32_t>(r) >> 1) & 3u)) << 4);
-      st_shared_v2(a + off, hi);
-      st_shared_v2(a + hpad * 64u + off, lo);
+    // hpad is a multiple of 8, so the lo row hpad + r has the same swizzle phase as row r
+    uint8_t* at = dst + (ch >> 3) * hpad * 128 + r * 64 + ((((ch & 7) >> 1) ^ ((r >> 1) & 3)) << 4) + (ch & 1) * 8;
+    *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+    *reinterpret_cast<uint2*>(at + hpad * 64) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+  }
+  if (lane == 0) {
+    // no such head, or a row without keys: weight 0.  A non-finite row gets a NaN factor (its codes
+    // would saturate) and makes the request's sums NaN.
+    float2 hf = make_float2(0.f, -INFINITY);
+    if (lse != -INFINITY) {
+      hf.x = m >= 0x7F80u ? __uint_as_float(0x7FC00000u)
+                          : p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+      hf.y = -lse * 1.4426950408889634f;
     }
-    // non-finite rows: a NaN factor makes the request's sums NaN (the codes above would saturate)
-    if (lane == 0) {
-      const int i = static_cast<int>(p.divG.div(w.item)), g = w.item - i * p.G;
-      const float lse = r < heads ? p.lse[(static_cast<size_t>(w.b) * p.T + i) * p.H + g * ACC_HEADS + r] : -INFINITY;
-      float f = 0.f, nl = -INFINITY;                     // no such head, or a row without keys: weight 0
-      if (lse != -INFINITY) {
-        f = m >= 0x7F80u ? __uint_as_float(0x7FC00000u)
-                         : p.softmax_scale * 1.4426950408889634f *
-                               __uint_as_float(static_cast<uint32_t>(127 - (k >> 1)) << 23) *
-                               __uint_as_float(static_cast<uint32_t>(127 - (k - (k >> 1))) << 23);
-        nl = -lse * 1.4426950408889634f;
-      }
-      st_shared_v2(base + ACC_SH + r * 8, make_uint2(__float_as_uint(f), __float_as_uint(nl)));
-    }
+    reinterpret_cast<float2*>(dst + ACC_COLS * hpad * 128)[r] = hf;
   }
 }
 
@@ -270,22 +295,17 @@ __global__ void __launch_bounds__(ACC_THREADS, 1) mla_accumulate_kernel(const __
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem + ACC_SMISC + 4);
   int* range = reinterpret_cast<int*>(smem + ACC_SMISC + 16);     // first request, its first tile
-  long long* tot = reinterpret_cast<long long*>(smem + ACC_SQ);   // scan scratch (before q is written)
+  long long* tot = reinterpret_cast<long long*>(smem + ACC_SMISC + 64);   // scan scratch
   auto bar = [&](uint32_t i) { return base + ACC_SBAR + 8 * i; };
-
+  if (base - raw > ACC_SMEM_ALLOC - ACC_SMEM) {          // the map needs a base within 255 bytes of 1 KB
+    if (threadIdx.x == 0) raise_status(p.status, STATUS_LAYOUT);
+    return;
+  }
   if (threadIdx.x == 0) {
-    for (uint32_t i = 0; i < ACC_SLOTS; ++i) {
-      ptx::mbar_init(bar(AB_K_FULL + i), 1);
-      ptx::mbar_init(bar(AB_K_EMPTY + i), 1);
+    for (uint32_t i = 0; i < ACC_BARS; ++i) {
+      const bool many = (i >= AB_ACC_EMPTY && i < AB_ACC_EMPTY + 2) || (i >= AB_H_EMPTY && i < AB_H_EMPTY + 2);
+      ptx::mbar_init(bar(i), many ? 128 : 1);
     }
-    for (uint32_t i = 0; i < 2; ++i) {
-      ptx::mbar_init(bar(AB_ACC_FULL + i), 1);
-      ptx::mbar_init(bar(AB_ACC_EMPTY + i), 128);
-    }
-    ptx::mbar_init(bar(AB_Q_FULL), 32 * ACC_Q_WARPS);
-    ptx::mbar_init(bar(AB_Q_EMPTY), 1);
-    ptx::mbar_init(bar(AB_ITEM_DONE), 128);
-    ptx::mbar_init(bar(AB_DRAIN), 1);
     *abort = 0u;
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&p.tmap_k);
@@ -331,85 +351,117 @@ __global__ void __launch_bounds__(ACC_THREADS, 1) mla_accumulate_kernel(const __
   const uint64_t lim = p.wait_limit_ns;
   const int t0 = range[1];
   AccWalker w(range[0], t0, r1 - r0);
-  auto wait = [&](uint32_t b, uint32_t parity) {         // whole warp, all or none
-    return __all_sync(0xffffffffu, wait_bar(b, parity, abort, p.status, 0, lim)) != 0;
-  };
-  auto poll = [&](uint32_t b, uint32_t parity) {
-    return __all_sync(0xffffffffu, poll_bar(b, parity, abort, p.status, 0, lim)) != 0;
-  };
+  // Every thread waits for itself: a wait that gives up marks the CTA, and the other roles' waits end.
+  auto wait = [&](uint32_t b, uint32_t parity) { return spin_bar(b, parity, abort, p.status, lim); };
 
   if (warp == 0) {
-    // ------------------------------------------------------------------ producer
+    // ------------------------------------------------------------------ K producer: lane r, page run r
     uint32_t n = 0;                                      // columns issued
-    const int runs = ACC_BN / p.box_rows;
+    const uint32_t runs = ACC_BN / p.box_rows;
+    auto find = [&](int b, int j, int& row) {            // where this lane's run of tile j lies
+      const uint32_t t = static_cast<uint32_t>(j) * ACC_BN + lane * p.box_rows;
+      if (static_cast<uint32_t>(lane) >= runs || t >= acc_length(p, b) + p.T) return false;
+      const uint32_t page = p.divP.div(t);
+      const uint32_t blk = p.lut[static_cast<size_t>(b) * p.max_pages + page];
+      row = static_cast<int>((static_cast<uint64_t>(blk) * p.KVD * p.NL + p.layer) * p.P + (t - page * p.P));
+      return blk < static_cast<uint32_t>(p.NB);          // else the epilogue flags it and leaves its keys
+    };
     bool live = w.start(p, t0);
+    int row = 0;
+    bool have = live && find(w.b, w.j, row);
     while (live) {
-      const uint32_t t = static_cast<uint32_t>(w.j) * ACC_BN + lane * p.box_rows;
-      bool have = lane < runs && t < acc_length(p, w.b) + p.T;
-      int row = 0;
-      if (have) {
-        const uint32_t page = p.divP.div(t);
-        const uint32_t blk = p.lut[static_cast<size_t>(w.b) * p.max_pages + page];
-        have = blk < static_cast<uint32_t>(p.NB);        // the epilogue flags it and leaves its keys
-        row = static_cast<int>((static_cast<uint64_t>(blk) * p.KVD * p.NL + p.layer) * p.P + (t - page * p.P));
-      }
+      const bool more = w.next(p);
+      int next_row = 0;
+      const bool next_have = more && find(w.b, w.j, next_row);   // in flight while this tile is issued
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, have)) * p.box_rows * 64u;
-      for (int c = 0; c < ACC_COLS; ++c, ++n) {
+      for (int c = 0; c < ACC_COLS && live; ++c, ++n) {
         const uint32_t s = n % ACC_SLOTS, use = n / ACC_SLOTS;
-        if (!wait(bar(AB_K_EMPTY + s), (use & 1) ^ 1)) { live = false; break; }
+        const bool ok = wait(bar(AB_K_EMPTY + s), (use & 1) ^ 1);
+        if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
         if (lane == 0) ptx::mbar_arrive_expect_tx(bar(AB_K_FULL + s), bytes);
         __syncwarp();
         if (have)
           ptx::tma_load_3d(base + ACC_SK + s * ACC_SLOT_BYTES + lane * p.box_rows * 64u, &p.tmap_k, 0, row, c,
                            bar(AB_K_FULL + s));
       }
-      live = live && w.next(p);
+      live = live && more;
+      row = next_row;
+      have = next_have;
     }
     // no copy may land after the CTA is gone (also on an aborted call)
     for (uint32_t s = 0; s < ACC_SLOTS && s < n; ++s)
       drain_bar(bar(AB_K_FULL + s), ((n - 1 - s) / ACC_SLOTS) & 1, lim);
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
-    uint32_t n = 0, tile = 0, items = 0;
-    bool live = w.start(p, t0);
-    while (live) {
-      const int g = w.item - static_cast<int>(p.divG.div(w.item)) * p.G;
-      const int hpad = (min(p.H - g * ACC_HEADS, ACC_HEADS) + 7) & ~7;
-      const uint32_t idesc = ptx::idesc_e4m3_f32(ACC_BN, 2 * hpad, false, false);
-      const uint32_t col_bytes = static_cast<uint32_t>(hpad) * 128u;
-      if (w.first_of_item()) {
-        if (!poll(bar(AB_Q_FULL), items & 1)) break;
-        ++items;
-      }
-      const uint32_t d = tbase + (tile & 1) * 256;
-      if (!poll(bar(AB_ACC_EMPTY + (tile & 1)), ((tile >> 1) & 1) ^ 1)) break;
-      ptx::tc_fence_after();
-      for (int c = 0; c < ACC_COLS; ++c, ++n) {
-        const uint32_t s = n % ACC_SLOTS;
-        if (!poll(bar(AB_K_FULL + s), (n / ACC_SLOTS) & 1)) { live = false; break; }
+    // ------------------------------------------------------------------ MMA issuer (one thread)
+    if (ptx::elect_one()) {
+      const uint32_t col = acc_hpad(p, 0) * 128;         // a column's place is the same for every head group
+      uint32_t s = 0, use = 0, tile = 0, items = 0;
+      bool live = w.start(p, t0);
+      while (live) {
+        const int g = w.item - static_cast<int>(p.divG.div(w.item)) * p.G;
+        const uint32_t hpad = acc_hpad(p, g);
+        const uint32_t idesc = ptx::idesc_e4m3_f32(ACC_BN, 2 * hpad, false, false);
+        const uint64_t a0 = ptx::smem_desc(base + ACC_SK, 16, 512, ptx::SW_64B);
+        uint64_t b = ptx::smem_desc(base + ACC_SQ, 16, 512, ptx::SW_64B);
+        const bool first = w.first_of_item(), last = w.last_of_item();
+        const uint32_t d = tbase + (tile & 1) * 256;
+        if (!wait(bar(AB_ACC_EMPTY + (tile & 1)), ((tile >> 1) & 1) ^ 1)) break;
         ptx::tc_fence_after();
-        if (ptx::elect_one()) {
-          const uint64_t a = ptx::smem_desc(base + ACC_SK + s * ACC_SLOT_BYTES, 16, 512, ptx::SW_64B);
-          const uint64_t b = ptx::smem_desc(base + ACC_SQ + c * col_bytes, 16, 512, ptx::SW_64B);
+        for (int c = 0; c < ACC_COLS; ++c) {
+          if (first && !wait(bar(AB_Q_FULL + c), items & 1)) { live = false; break; }
+          if (!wait(bar(AB_K_FULL + s), use & 1)) { live = false; break; }
+          ptx::tc_fence_after();
+          const uint64_t a = a0 + s * (ACC_SLOT_BYTES >> 4);
           mma_ss_e4m3(d, a, b, idesc, c > 0);
           mma_ss_e4m3(d, a + 2, b + 2, idesc, 1);        // the column's second 32 dims: + 32 bytes
           ptx::mma_commit(bar(AB_K_EMPTY + s));
+          if (last) ptx::mma_commit(bar(AB_Q_EMPTY + c));
+          b += col >> 4;
+          if (++s == ACC_SLOTS) { s = 0; ++use; }
         }
-        __syncwarp();
-      }
-      if (!live) break;
-      if (ptx::elect_one()) {
+        if (!live) break;
         ptx::mma_commit(bar(AB_ACC_FULL + (tile & 1)));
-        if (w.last_of_item()) ptx::mma_commit(bar(AB_Q_EMPTY));
+        items += last;
+        ++tile;
+        live = w.next(p);
       }
-      __syncwarp();
-      ++tile;
-      live = w.next(p);
+      ptx::mma_commit(bar(AB_DRAIN));
+      drain_bar(bar(AB_DRAIN), 0, lim);
     }
-    if (ptx::elect_one()) ptx::mma_commit(bar(AB_DRAIN));
     __syncwarp();
-    drain_bar(bar(AB_DRAIN), 0, lim);
-  } else if (warp >= ACC_EPI_WARP0 && warp < ACC_EPI_WARP0 + 4) {
+  } else if (warp == ACC_Q_WARP) {
+    // ------------------------------------------------------------------ q producer (one thread)
+    if (ptx::elect_one()) {
+      ptx::griddep_wait();                               // the split kernel has written the workspace
+      const uint32_t col = acc_hpad(p, 0) * 128;
+      uint32_t items = 0, cols = 0;
+      bool live = w.start(p, t0);
+      while (live) {
+        const int i = static_cast<int>(p.divG.div(w.item)), g = w.item - i * p.G;
+        const uint32_t hpad = acc_hpad(p, g);
+        const uint8_t* src = p.split + ((static_cast<long long>(w.b) * p.ni + i) * p.G + g) * p.item_bytes;
+        if (!wait(bar(AB_H_EMPTY + (items & 1)), ((items >> 1) & 1) ^ 1)) break;
+        ptx::mbar_arrive_expect_tx(bar(AB_H_FULL + (items & 1)), hpad * 8);
+        ptx::bulk_load(base + ACC_SH + (items & 1) * ACC_HEADS * 8, src + ACC_COLS * hpad * 128, hpad * 8,
+                       bar(AB_H_FULL + (items & 1)));
+        cols = 0;
+        ++items;
+        for (; cols < ACC_COLS; ++cols) {
+          if (!wait(bar(AB_Q_EMPTY + cols), (items & 1))) { live = false; break; }
+          ptx::mbar_arrive_expect_tx(bar(AB_Q_FULL + cols), hpad * 128);
+          ptx::bulk_load(base + ACC_SQ + cols * col, src + cols * hpad * 128, hpad * 128, bar(AB_Q_FULL + cols));
+        }
+        live = live && w.next_item(p);
+      }
+      // the copies of the last item (and, of columns not reached, of the one before) have landed
+      for (uint32_t c = 0; c < ACC_COLS; ++c) {
+        const uint32_t done = items - (c < cols ? 0 : 1);   // times column c was loaded
+        if (items > 0 && done > 0) drain_bar(bar(AB_Q_FULL + c), (done - 1) & 1, lim);
+      }
+      for (uint32_t x = 0; x < 2 && x < items; ++x) drain_bar(bar(AB_H_FULL + ((items - 1 - x) & 1)), ((items - 1 - x) >> 1) & 1, lim);
+    }
+    __syncwarp();
+  } else if (warp >= ACC_EPI_WARP0) {
     // ------------------------------------------------------------------ epilogue
     const int r = threadIdx.x - 32 * ACC_EPI_WARP0;      // the tile's key = tensor-memory lane
     const uint32_t quad = static_cast<uint32_t>(warp - ACC_EPI_WARP0) << 21;
@@ -425,13 +477,14 @@ __global__ void __launch_bounds__(ACC_THREADS, 1) mla_accumulate_kernel(const __
       // the next tile's scale and running sum are on their way while this tile is summed
       const AccKey nxt = live ? acc_key(p, w.b, w.item, w.j, r) : AccKey{0.f, 0.f, nullptr};
       const int i = static_cast<int>(p.divG.div(cur.item)), g = cur.item - i * p.G;
-      const int hpad = (min(p.H - g * ACC_HEADS, ACC_HEADS) + 7) & ~7;
-      if (cur.first_of_item() && !wait(bar(AB_Q_FULL), items & 1)) break;   // head factors are written
-      if (!wait(bar(AB_ACC_FULL + (tile & 1)), (tile >> 1) & 1)) break;
+      const uint32_t hpad = acc_hpad(p, g);
+      bool ok = !cur.first_of_item() || wait(bar(AB_H_FULL + (items & 1)), (items >> 1) & 1);
+      ok = ok && wait(bar(AB_ACC_FULL + (tile & 1)), (tile >> 1) & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
       ptx::tc_fence_after();
-      const uint32_t d = tbase + quad + (tile & 1) * 256, hf = base + ACC_SH;
+      const uint32_t d = tbase + quad + (tile & 1) * 256, hf = base + ACC_SH + (items & 1) * ACC_HEADS * 8;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      int h = 0;
+      uint32_t h = 0;
       for (; h + 32 <= hpad; h += 32) {
         uint32_t hi[32], lo[32];
         ptx::tmem_ld32(d + h, hi);
@@ -449,50 +502,16 @@ __global__ void __launch_bounds__(ACC_THREADS, 1) mla_accumulate_kernel(const __
       ptx::tc_fence_before();
       ptx::mbar_arrive(bar(AB_ACC_EMPTY + (tile & 1)));
       if (cur.last_of_item()) {
-        ptx::mbar_arrive(bar(AB_ITEM_DONE));
+        ptx::mbar_arrive(bar(AB_H_EMPTY + (items & 1)));
         ++items;
       }
       if (key.dst) {
         const uint32_t t = static_cast<uint32_t>(cur.j) * ACC_BN + r;
-        const float add = t <= acc_length(p, cur.b) + i ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
-        *key.dst = (cur.item == 0 ? key.base : *key.dst) + add;
+        const float add = t <= acc_length(p, cur.b) + p.i0 + i ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
+        *key.dst = (cur.item == 0 && p.i0 == 0 ? key.base : *key.dst) + add;
       }
       key = nxt;
       ++tile;
-    }
-  } else if (warp >= ACC_Q_WARP0) {
-    // ------------------------------------------------------------------ q split
-    const int wq = warp - ACC_Q_WARP0;
-    uint32_t items = 0;
-    bool live = w.start(p, t0);
-    while (live) {
-      const int i = static_cast<int>(p.divG.div(w.item)), g = w.item - i * p.G;
-      const int heads = min(p.H - g * ACC_HEADS, ACC_HEADS), hpad = (heads + 7) & ~7;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + ((static_cast<size_t>(w.b) * p.T + i) * p.H + g * ACC_HEADS) * HEAD_DIM);
-      bool freed = items == 0;
-      for (int r0 = wq; r0 < hpad; r0 += 4 * ACC_Q_WARPS) {
-        uint4 v[4][3];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = r0 + u * ACC_Q_WARPS;
-#pragma unroll
-          for (int c = 0; c < 3; ++c)
-            v[u][c] = r < heads && lane + 32 * c < HEAD_DIM / 8 ? src[static_cast<size_t>(r) * (HEAD_DIM / 8) + lane + 32 * c]
-                                                               : make_uint4(0, 0, 0, 0);
-        }
-        if (!freed) {   // the last item's MMAs have read q, and its epilogue the head factors
-          if (!wait(bar(AB_Q_EMPTY), (items - 1) & 1) || !wait(bar(AB_ITEM_DONE), (items - 1) & 1)) { live = false; break; }
-          freed = true;
-        }
-        acc_write_q(p, w, base, wq, lane, heads, hpad, v, r0);
-      }
-      if (!live) break;
-      if (!freed && (!wait(bar(AB_Q_EMPTY), (items - 1) & 1) || !wait(bar(AB_ITEM_DONE), (items - 1) & 1))) break;
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(bar(AB_Q_FULL));
-      ++items;
-      live = w.next_item(p);
     }
   }
   ptx::tc_fence_before();

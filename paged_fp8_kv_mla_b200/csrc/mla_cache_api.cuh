@@ -97,6 +97,30 @@ mla_status_t make_row_map(CUtensorMap* map, const void* blocks, uint64_t rows, u
   return MLA_OK;
 }
 
+// The split q of the accumulated weights: an item's bytes, and the query tokens that one launch takes
+// (long prompts run in several launches, so that the workspace stays at 256 MB unless one token of the
+// batch needs more).
+struct AccPlan {
+  uint32_t item_bytes, heads;
+  int tokens;
+  uint64_t total;
+};
+
+mla_status_t acc_plan(int64_t B, int64_t T, int64_t H, AccPlan* out) {
+  AccPlan a{};
+  const int64_t G = (H + mla::ACC_HEADS - 1) / mla::ACC_HEADS;
+  a.heads = static_cast<uint32_t>(((H < mla::ACC_HEADS ? H : mla::ACC_HEADS) + 7) / 8 * 8);
+  a.item_bytes = a.heads * (mla::ACC_COLS * 128 + 8);
+  if (B * G > (1ll << 24)) return fail(MLA_ERR_UNSUPPORTED, "too many (request, head group) items");
+  const int64_t token = B * G * a.item_bytes;
+  int64_t tokens = (256ll << 20) / token;
+  tokens = tokens < 1 ? 1 : tokens > T ? T : tokens;
+  a.tokens = static_cast<int>(tokens);
+  a.total = static_cast<uint64_t>(token) * tokens;
+  *out = a;
+  return MLA_OK;
+}
+
 // How a multi-head decode is laid out (the rules the kernel's header comment describes).
 struct MhaPlan {
   int R, hg, mt, kw, head_groups, row_groups, tile, box_rows, stages, NC, one_item;
@@ -196,7 +220,8 @@ mla_status_t mla_accumulate_weights_fp8(const void* q, const float* lse, const v
                                         const uint32_t* scales_lookup_table, uint32_t max_prompt_length,
                                         uint32_t max_cache_length, uint32_t layer_idx, float softmax_scale,
                                         const mla_paged_shape_t* shape, const float* scores, int64_t scores_stride,
-                                        float* out, int64_t out_stride, cudaStream_t stream) {
+                                        float* out, int64_t out_stride, void* workspace, uint64_t workspace_bytes,
+                                        cudaStream_t stream) {
   mla::DecodeParams d{};
   uint64_t rows = 0;
   mla_status_t st = check_cache(blocks, scales, cache_lengths, lookup_table, max_prompt_length, max_cache_length,
@@ -222,6 +247,15 @@ mla_status_t mla_accumulate_weights_fp8(const void* q, const float* lse, const v
   p.box_rows = gcd_int(d.P, mla::ACC_BN);
   st = make_row_map(&p.tmap_k, blocks, rows, mla::HEAD_DIM, 64, p.box_rows, 1);
   if (st != MLA_OK) return st;
+  AccPlan plan{};
+  st = acc_plan(d.B, d.T, d.H, &plan);
+  if (st != MLA_OK) return st;
+  if (!workspace || workspace_bytes < plan.total)
+    return fail(MLA_ERR_WORKSPACE, "the call needs a workspace of %llu bytes (mla_accumulate_workspace_bytes)",
+                static_cast<unsigned long long>(plan.total));
+  if (!aligned16(workspace)) return fail(MLA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  p.split = static_cast<uint8_t*>(workspace);
+  p.item_bytes = plan.item_bytes;
   p.q = static_cast<const uint16_t*>(q);
   p.lse = lse;
   p.scales = scales;
@@ -255,9 +289,36 @@ mla_status_t mla_accumulate_weights_fp8(const void* q, const float* lse, const v
   }
   const uint64_t most = static_cast<uint64_t>(d.B) * ((need + mla::ACC_BN - 1) / mla::ACC_BN);
   const unsigned grid = static_cast<unsigned>(most < static_cast<uint64_t>(sms) ? most : sms);
-  mla::mla_accumulate_kernel<<<grid, mla::ACC_THREADS, mla::ACC_SMEM_ALLOC, stream>>>(p);
-  MLA_CUDA(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(mla::ACC_THREADS);
+  cfg.dynamicSmemBytes = mla::ACC_SMEM_ALLOC;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  for (p.i0 = 0; p.i0 < d.T; p.i0 += plan.tokens) {
+    p.ni = d.T - p.i0 < plan.tokens ? d.T - p.i0 : plan.tokens;
+    const uint64_t warps = static_cast<uint64_t>(d.B) * p.ni * d.G * plan.heads;
+    mla::mla_split_q_kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, stream>>>(p);
+    MLA_CUDA(cudaGetLastError());
+    MLA_CUDA(cudaLaunchKernelEx(&cfg, mla::mla_accumulate_kernel, p));
+  }
   return MLA_OK;
+}
+
+mla_status_t mla_accumulate_workspace_bytes(uint32_t max_prompt_length, const mla_paged_shape_t* s, uint64_t* bytes) {
+  if (!s || !bytes) return fail(MLA_ERR_INVALID_ARG, "shape and bytes must be non-NULL");
+  *bytes = 0;
+  if (s->batch < 0 || s->num_q_heads < 1 || max_prompt_length < 1)
+    return fail(MLA_ERR_INVALID_ARG, "non-positive dimension in shape, or no query tokens");
+  if (s->batch == 0) return MLA_OK;
+  AccPlan plan{};
+  const mla_status_t st = acc_plan(s->batch, static_cast<int64_t>(max_prompt_length), s->num_q_heads, &plan);
+  if (st == MLA_OK) *bytes = plan.total;
+  return st;
 }
 
 mla_status_t mla_select_keys(const float* scores, int64_t scores_stride, const uint32_t* lengths, int32_t batch,
