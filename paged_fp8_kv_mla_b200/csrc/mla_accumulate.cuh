@@ -28,11 +28,15 @@
 // Work split.  All requests' tiles of 128 keys laid end to end are cut into equal contiguous ranges,
 // one per CTA (one CTA per SM).  A key belongs to one CTA for all query tokens and head groups, so
 // sums are formed in a fixed order by one thread: no atomics, and the result does not depend on the
-// launch.  K moves through a ring of ten 8 KB slots, one 64-dim column of a tile each, filled by TMA
-// (one box per page run) and released by tcgen05.commit, so loads, MMAs and the exponentials of the
-// tile before overlap.  q is replaced column by column as the last MMAs of an item release it.
+// launch.  K moves column by column, four of 128 dims (128-byte swizzle) and one of 64 per tile, through
+// two rings of slots filled by TMA (one box per page run) and released by tcgen05.commit, so loads, MMAs
+// and the exponentials of the tile before overlap.  A column's hand-over costs the producer about 330
+// cycles whatever its width (traced), and a tile takes 3200 at HBM rate: five columns fit, nine of 64
+// dims did not.  q is replaced column by column as the last MMAs of an item release it.  Two groups of
+// epilogue warps take the even and the odd tiles of a request (one takes 3000 cycles a tile).
 //
-// Warps: 0 K producer, 1 MMA issuer and TMEM owner, 2 q producer, 4-7 epilogue (lane quadrants 0-3).
+// Warps: 0 K producer, 1 MMA issuer and TMEM owner, 2 q producer, 4-7 and 8-11 epilogue (each the lane
+// quadrants 0-3, for tiles of one parity).
 #pragma once
 #include <cstdint>
 #include "mla_kernels.cuh"
@@ -40,7 +44,8 @@
 namespace mla {
 
 struct AccumulateParams {
-  CUtensorMap tmap_k;              // blocks as {64 bytes, rows, 9 columns}, box = box_rows rows of a column
+  CUtensorMap tmap_k;              // dims 0..511 of blocks as {128 bytes, rows, 4 columns}, box = box_rows rows of one
+  CUtensorMap tmap_r;              // dims 512..575 as {64 bytes, rows, 1}
   const uint16_t* q;               // bf16 bits [B, T, H, 576]
   const float* lse;                // [B, T, H], natural log
   uint8_t* split;                  // workspace: per item, q's columns as the MMA reads them, then head factors
@@ -63,30 +68,37 @@ struct AccumulateParams {
 
 constexpr int ACC_BN = 128;                       // keys per tile (MMA M)
 constexpr int ACC_HEADS = 128;                    // heads per item (MMA N = 2 x heads)
-constexpr int ACC_COLS = HEAD_DIM / 64;           // 9 columns of 64 dims
-constexpr int ACC_THREADS = 256;
+constexpr int ACC_COLS = 5;                       // columns of a key: 4 of 128 dims, 1 of 64
+constexpr int ACC_THREADS = 384;
 constexpr int ACC_Q_WARP = 2;
 constexpr int ACC_EPI_WARP0 = 4;
-constexpr int ACC_SLOTS = 10;
-constexpr uint32_t ACC_SLOT_BYTES = ACC_BN * 64;
-constexpr uint32_t ACC_SQ = 0;                    // [9 columns][2 x heads rows (hi, then lo)][64 B]
-constexpr uint32_t ACC_SK = ACC_COLS * 2 * ACC_HEADS * 64;
-constexpr uint32_t ACC_SH = ACC_SK + ACC_SLOTS * ACC_SLOT_BYTES;   // [2][128] {factor, -lse log2 e}
+constexpr int ACC_MAX_WIDE = 12, ACC_MAX_NARROW = 4;   // slots of the two rings
+constexpr uint32_t ACC_WIDE_BYTES = ACC_BN * 128, ACC_NARROW_BYTES = ACC_BN * 64;
+// Shared memory: head factors, barriers, scalars; then q, each column [2 x heads rows (hi, then lo)], and
+// the rings in what is left (4 and 2 slots at 128 heads, up to 12 and 4 for few heads).
+constexpr uint32_t ACC_SH = 0;                    // [2][128] {factor, -lse log2 e}
 constexpr uint32_t ACC_SBAR = ACC_SH + 2 * ACC_HEADS * 8;
 constexpr uint32_t ACC_SMISC = ACC_SBAR + 512;
-constexpr uint32_t ACC_SMEM = ACC_SMISC + 256;
+constexpr uint32_t ACC_SQ = 3072;
 constexpr uint32_t ACC_SMEM_ALLOC = 232448;
-static_assert(ACC_SMEM + 255 <= ACC_SMEM_ALLOC, "shared memory map exceeds 227 KB");
+static_assert(ACC_SMISC + 256 <= ACC_SQ && ACC_SQ % 1024 == 0, "scalars overlap q");
+__host__ __device__ constexpr uint32_t acc_wide_slots(uint32_t hpad) {
+  uint32_t n = ACC_MAX_WIDE;
+  while (n * ACC_WIDE_BYTES + (n / 4 + 1) * ACC_NARROW_BYTES > ACC_SMEM_ALLOC - ACC_SQ - hpad * 2 * HEAD_DIM) --n;
+  return n;
+}
+static_assert(acc_wide_slots(ACC_HEADS) == 4 && ACC_MAX_WIDE / 4 + 1 == ACC_MAX_NARROW, "rings of K slots");
 
 enum AccBar : uint32_t {
-  AB_K_FULL = 0,                    // [10] producer's expect_tx arrival + the column's bytes
-  AB_K_EMPTY = ACC_SLOTS,           // [10] commit: the column's MMAs have read it
-  AB_ACC_FULL = 2 * ACC_SLOTS,      // [2] commit: a tile's products are in tensor memory
+  // slot x of the wide ring, then slot x - ACC_MAX_WIDE of the narrow one:
+  AB_K_FULL = 0,                    // producer's expect_tx arrival + the column's bytes
+  AB_K_EMPTY = ACC_MAX_WIDE + ACC_MAX_NARROW,   // commit: the column's MMAs have read it
+  AB_ACC_FULL = 2 * AB_K_EMPTY,     // [2] commit: a tile's products are in tensor memory (by tile parity)
   AB_ACC_EMPTY = AB_ACC_FULL + 2,   // [2] 128 epilogue threads have read them
-  AB_Q_FULL = AB_ACC_EMPTY + 2,     // [9] a column of an item's q is in (bytes)
-  AB_Q_EMPTY = AB_Q_FULL + ACC_COLS,   // [9] commit: the item's last MMAs on the column are done
+  AB_Q_FULL = AB_ACC_EMPTY + 2,     // [5] a column of an item's q is in (bytes)
+  AB_Q_EMPTY = AB_Q_FULL + ACC_COLS,   // [5] commit: the item's last MMAs on the column are done
   AB_H_FULL = AB_Q_EMPTY + ACC_COLS,   // [2] an item's head factors are in (bytes)
-  AB_H_EMPTY = AB_H_FULL + 2,       // [2] 128 epilogue threads have read them
+  AB_H_EMPTY = AB_H_FULL + 2,       // [2] 256 epilogue threads have read them
   AB_DRAIN = AB_H_EMPTY + 2,        // commit at exit
   ACC_BARS
 };
@@ -108,19 +120,21 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Bounded wait on an mbarrier phase that polls without sleeping: for roles whose every wait sits on the
-// path of a tile (a thread suspended in try_wait resumes hundreds of cycles late).  Looks at the clock
-// and at the abort flag every 256 polls only.
-__device__ __forceinline__ bool spin_bar(uint32_t addr, uint32_t parity, volatile uint32_t* abort, unsigned int* status,
-                                         uint64_t limit) {
-  if (ptx::mbar_test_wait(addr, parity)) return true;
-  const uint64_t t0 = ptx::globaltimer();
+// Bounded wait on an mbarrier phase in try_wait, which suspends the thread: threads that poll with
+// test_wait keep the barrier unit busy (14 cycles a poll, several times that where the lanes of a warp
+// poll different barriers) and made every other role's waits four times as long (210 instead of 50
+// cycles on a phase that was complete).  The clock and the abort flag are looked at every 64 tries.
+__device__ __forceinline__ bool try_bar(uint32_t addr, uint32_t parity, volatile uint32_t* abort, unsigned int* status,
+                                        uint64_t limit) {
+  if (ptx::mbar_try_wait(addr, parity)) return true;
+  uint64_t t0 = 0;
   for (uint32_t n = 1;; ++n) {
-    if (ptx::mbar_test_wait(addr, parity)) return true;
-    if ((n & 255u) == 0) {
-      if (*abort) return false;
-      if (ptx::globaltimer() - t0 > limit) return wait_gave_up(abort, status, 0);
-    }
+    if (ptx::mbar_try_wait(addr, parity)) return true;
+    if (n & 63u) continue;
+    if (*abort) return false;
+    const uint64_t t = ptx::globaltimer();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > limit) return wait_gave_up(abort, status, 0);
   }
 }
 
@@ -216,8 +230,9 @@ __device__ __forceinline__ void acc_heads(const uint32_t (&hi)[W], const uint32_
 }
 
 // ------------------------------------------------------------------ q split
-// Workspace of an item ((b * ni + i) * G + g): 9 columns of 2 hpad rows (hi of each head, then lo) of
-// 64 bytes in the 64-byte swizzle, then {factor, -lse log2 e} of each head; hpad heads, a multiple of 8.
+// Workspace of an item ((b * ni + i) * G + g): 4 columns of 2 hpad rows (hi of each head, then lo) of
+// 128 bytes in the 128-byte swizzle, one of 64 bytes in the 64-byte swizzle, then {factor, -lse log2 e}
+// of each head; hpad heads, a multiple of 8.
 __device__ __forceinline__ uint32_t acc_hpad(const AccumulateParams& p, int g) {
   return (min(p.H - g * ACC_HEADS, ACC_HEADS) + 7) & ~7;
 }
@@ -270,9 +285,11 @@ __global__ void __launch_bounds__(256) mla_split_q_kernel(const __grid_constant_
       lo[x] = ptx::e4m3x2_rn_satfinite_f16x2(mul_f16x2(rest, 0x4C004C00u));   // x 16
     }
     // hpad is a multiple of 8, so the lo row hpad + r has the same swizzle phase as row r
-    uint8_t* at = dst + (ch >> 3) * hpad * 128 + r * 64 + ((((ch & 7) >> 1) ^ ((r >> 1) & 3)) << 4) + (ch & 1) * 8;
+    const bool wide = ch < 64;
+    const uint32_t unit = (ch >> 1) & 7, width = wide ? 128 : 64;
+    uint8_t* at = dst + (ch >> 4) * hpad * 256 + r * width + ((unit ^ (wide ? r & 7 : (r >> 1) & 3)) << 4) + (ch & 1) * 8;
     *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-    *reinterpret_cast<uint2*>(at + hpad * 64) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+    *reinterpret_cast<uint2*>(at + hpad * width) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
   }
   if (lane == 0) {
     // no such head, or a row without keys: weight 0.  A non-finite row gets a NaN factor (its codes
@@ -283,32 +300,35 @@ __global__ void __launch_bounds__(256) mla_split_q_kernel(const __grid_constant_
                           : p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
       hf.y = -lse * 1.4426950408889634f;
     }
-    reinterpret_cast<float2*>(dst + ACC_COLS * hpad * 128)[r] = hf;
+    reinterpret_cast<float2*>(dst + hpad * 2 * HEAD_DIM)[r] = hf;
   }
 }
 
 __global__ void __launch_bounds__(ACC_THREADS, 1) mla_accumulate_kernel(const __grid_constant__ AccumulateParams p) {
   extern __shared__ uint8_t acc_smem_raw[];
-  const uint32_t raw = ptx::smem_u32(acc_smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* smem = acc_smem_raw + (base - raw);
+  const uint32_t base = ptx::smem_u32(acc_smem_raw);
+  uint8_t* smem = acc_smem_raw;
+  const uint32_t col = acc_hpad(p, 0) * 256;             // a q column's place is the same for every head group
+  const uint32_t wides = acc_wide_slots(acc_hpad(p, 0)), narrows = wides / 4 + 1;
+  const uint32_t ring = ACC_SQ + acc_hpad(p, 0) * 2 * HEAD_DIM, ring_n = ring + wides * ACC_WIDE_BYTES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem + ACC_SMISC + 4);
   int* range = reinterpret_cast<int*>(smem + ACC_SMISC + 16);     // first request, its first tile
   long long* tot = reinterpret_cast<long long*>(smem + ACC_SMISC + 64);   // scan scratch
   auto bar = [&](uint32_t i) { return base + ACC_SBAR + 8 * i; };
-  if (base - raw > ACC_SMEM_ALLOC - ACC_SMEM) {          // the map needs a base within 255 bytes of 1 KB
+  if (base & 1023u) {                                    // the swizzled columns start at multiples of 1 KB
     if (threadIdx.x == 0) raise_status(p.status, STATUS_LAYOUT);
     return;
   }
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < ACC_BARS; ++i) {
-      const bool many = (i >= AB_ACC_EMPTY && i < AB_ACC_EMPTY + 2) || (i >= AB_H_EMPTY && i < AB_H_EMPTY + 2);
-      ptx::mbar_init(bar(i), many ? 128 : 1);
+      const bool acc = i >= AB_ACC_EMPTY && i < AB_ACC_EMPTY + 2, heads = i >= AB_H_EMPTY && i < AB_H_EMPTY + 2;
+      ptx::mbar_init(bar(i), acc ? 128 : heads ? 256 : 1);
     }
     *abort = 0u;
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&p.tmap_k);
+    ptx::prefetch_tmap(&p.tmap_r);
   }
   if (warp == 1) {
     ptx::tmem_alloc(base + ACC_SMISC, 512);
@@ -352,11 +372,11 @@ __global__ void __launch_bounds__(ACC_THREADS, 1) mla_accumulate_kernel(const __
   const int t0 = range[1];
   AccWalker w(range[0], t0, r1 - r0);
   // Every thread waits for itself: a wait that gives up marks the CTA, and the other roles' waits end.
-  auto wait = [&](uint32_t b, uint32_t parity) { return spin_bar(b, parity, abort, p.status, lim); };
+  auto wait = [&](uint32_t b, uint32_t parity) { return try_bar(b, parity, abort, p.status, lim); };
 
   if (warp == 0) {
     // ------------------------------------------------------------------ K producer: lane r, page run r
-    uint32_t n = 0;                                      // columns issued
+    uint32_t wide = 0, wide_use = 0, narrow = 0, narrow_use = 0;   // the rings' next slots
     const uint32_t runs = ACC_BN / p.box_rows;
     auto find = [&](int b, int j, int& row) {            // where this lane's run of tile j lies
       const uint32_t t = static_cast<uint32_t>(j) * ACC_BN + lane * p.box_rows;
@@ -372,57 +392,98 @@ __global__ void __launch_bounds__(ACC_THREADS, 1) mla_accumulate_kernel(const __
     while (live) {
       const bool more = w.next(p);
       int next_row = 0;
-      const bool next_have = more && find(w.b, w.j, next_row);   // in flight while this tile is issued
-      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, have)) * p.box_rows * 64u;
-      for (int c = 0; c < ACC_COLS && live; ++c, ++n) {
-        const uint32_t s = n % ACC_SLOTS, use = n / ACC_SLOTS;
-        const bool ok = wait(bar(AB_K_EMPTY + s), (use & 1) ^ 1);
-        if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
-        if (lane == 0) ptx::mbar_arrive_expect_tx(bar(AB_K_FULL + s), bytes);
+      const bool next_have = more && find(w.b, w.j, next_row);   // looked up while this tile is issued
+      const uint32_t rows = __popc(__ballot_sync(0xffffffffu, have)) * p.box_rows;
+      for (int c = 0; c < ACC_COLS; ++c) {
+        const bool is_wide = c < ACC_COLS - 1;
+        const uint32_t x = is_wide ? wide : ACC_MAX_WIDE + narrow;
+        const uint32_t full = bar(AB_K_FULL + x);
+        if (!__all_sync(0xffffffffu, wait(bar(AB_K_EMPTY + x), ((is_wide ? wide_use : narrow_use) & 1) ^ 1))) {
+          live = false;
+          break;
+        }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(full, rows * (is_wide ? 128u : 64u));
         __syncwarp();
-        if (have)
-          ptx::tma_load_3d(base + ACC_SK + s * ACC_SLOT_BYTES + lane * p.box_rows * 64u, &p.tmap_k, 0, row, c,
-                           bar(AB_K_FULL + s));
+        if (is_wide) {
+          if (have)
+            ptx::tma_load_3d(base + ring + wide * ACC_WIDE_BYTES + lane * p.box_rows * 128u, &p.tmap_k, 0, row, c, full);
+          if (++wide == wides) {
+            wide = 0;
+            ++wide_use;
+          }
+        } else {
+          if (have)
+            ptx::tma_load_3d(base + ring_n + narrow * ACC_NARROW_BYTES + lane * p.box_rows * 64u, &p.tmap_r, 0, row, 0, full);
+          if (++narrow == narrows) {
+            narrow = 0;
+            ++narrow_use;
+          }
+        }
       }
       live = live && more;
       row = next_row;
       have = next_have;
     }
     // no copy may land after the CTA is gone (also on an aborted call)
-    for (uint32_t s = 0; s < ACC_SLOTS && s < n; ++s)
-      drain_bar(bar(AB_K_FULL + s), ((n - 1 - s) / ACC_SLOTS) & 1, lim);
+    for (uint32_t x = 0; x < wides; ++x) {
+      const uint32_t uses = wide_use + (x < wide);       // times slot x was filled
+      if (uses) drain_bar(bar(AB_K_FULL + x), (uses - 1) & 1, lim);
+    }
+    for (uint32_t x = 0; x < narrows; ++x) {
+      const uint32_t uses = narrow_use + (x < narrow);
+      if (uses) drain_bar(bar(AB_K_FULL + ACC_MAX_WIDE + x), (uses - 1) & 1, lim);
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer (one thread)
     if (ptx::elect_one()) {
-      const uint32_t col = acc_hpad(p, 0) * 128;         // a column's place is the same for every head group
-      uint32_t s = 0, use = 0, tile = 0, items = 0;
+      uint32_t wide = 0, wide_use = 0, narrow = 0, narrow_use = 0, items = 0;
+      uint32_t acc_use0 = 0, acc_use1 = 0;
       bool live = w.start(p, t0);
       while (live) {
         const int g = w.item - static_cast<int>(p.divG.div(w.item)) * p.G;
         const uint32_t hpad = acc_hpad(p, g);
         const uint32_t idesc = ptx::idesc_e4m3_f32(ACC_BN, 2 * hpad, false, false);
-        const uint64_t a0 = ptx::smem_desc(base + ACC_SK, 16, 512, ptx::SW_64B);
-        uint64_t b = ptx::smem_desc(base + ACC_SQ, 16, 512, ptx::SW_64B);
+        const uint64_t aw = ptx::smem_desc(base + ring, 16, 1024, ptx::SW_128B);
+        const uint64_t an = ptx::smem_desc(base + ring_n, 16, 512, ptx::SW_64B);
+        uint64_t b = ptx::smem_desc(base + ACC_SQ, 16, 1024, ptx::SW_128B);
+        const uint64_t bn = ptx::smem_desc(base + ACC_SQ + 4 * col, 16, 512, ptx::SW_64B);
         const bool first = w.first_of_item(), last = w.last_of_item();
-        const uint32_t d = tbase + (tile & 1) * 256;
-        if (!wait(bar(AB_ACC_EMPTY + (tile & 1)), ((tile >> 1) & 1) ^ 1)) break;
+        const uint32_t buf = w.j & 1, d = tbase + buf * 256;
+        if (!wait(bar(AB_ACC_EMPTY + buf), ((buf ? acc_use1 : acc_use0) & 1) ^ 1)) break;
         ptx::tc_fence_after();
+#pragma unroll
         for (int c = 0; c < ACC_COLS; ++c) {
+          const bool is_wide = c < ACC_COLS - 1;
+          const uint32_t x = is_wide ? wide : ACC_MAX_WIDE + narrow;
           if (first && !wait(bar(AB_Q_FULL + c), items & 1)) { live = false; break; }
-          if (!wait(bar(AB_K_FULL + s), use & 1)) { live = false; break; }
+          if (!wait(bar(AB_K_FULL + x), (is_wide ? wide_use : narrow_use) & 1)) { live = false; break; }
           ptx::tc_fence_after();
-          const uint64_t a = a0 + s * (ACC_SLOT_BYTES >> 4);
-          mma_ss_e4m3(d, a, b, idesc, c > 0);
-          mma_ss_e4m3(d, a + 2, b + 2, idesc, 1);        // the column's second 32 dims: + 32 bytes
-          ptx::mma_commit(bar(AB_K_EMPTY + s));
+          if (is_wide) {
+            const uint64_t a = aw + wide * (ACC_WIDE_BYTES >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_ss_e4m3(d, a + 2 * k, b + 2 * k, idesc, c + k > 0);   // 32 dims each
+            b += col >> 4;
+            if (++wide == wides) {
+              wide = 0;
+              ++wide_use;
+            }
+          } else {
+            const uint64_t a = an + narrow * (ACC_NARROW_BYTES >> 4);
+            mma_ss_e4m3(d, a, bn, idesc, 1);
+            mma_ss_e4m3(d, a + 2, bn + 2, idesc, 1);
+            if (++narrow == narrows) {
+              narrow = 0;
+              ++narrow_use;
+            }
+          }
+          ptx::mma_commit(bar(AB_K_EMPTY + x));
           if (last) ptx::mma_commit(bar(AB_Q_EMPTY + c));
-          b += col >> 4;
-          if (++s == ACC_SLOTS) { s = 0; ++use; }
         }
         if (!live) break;
-        ptx::mma_commit(bar(AB_ACC_FULL + (tile & 1)));
+        ptx::mma_commit(bar(AB_ACC_FULL + buf));
+        acc_use0 += !buf;
+        acc_use1 += buf;
         items += last;
-        ++tile;
         live = w.next(p);
       }
       ptx::mma_commit(bar(AB_DRAIN));
@@ -433,7 +494,6 @@ __global__ void __launch_bounds__(ACC_THREADS, 1) mla_accumulate_kernel(const __
     // ------------------------------------------------------------------ q producer (one thread)
     if (ptx::elect_one()) {
       ptx::griddep_wait();                               // the split kernel has written the workspace
-      const uint32_t col = acc_hpad(p, 0) * 128;
       uint32_t items = 0, cols = 0;
       bool live = w.start(p, t0);
       while (live) {
@@ -442,14 +502,15 @@ __global__ void __launch_bounds__(ACC_THREADS, 1) mla_accumulate_kernel(const __
         const uint8_t* src = p.split + ((static_cast<long long>(w.b) * p.ni + i) * p.G + g) * p.item_bytes;
         if (!wait(bar(AB_H_EMPTY + (items & 1)), ((items >> 1) & 1) ^ 1)) break;
         ptx::mbar_arrive_expect_tx(bar(AB_H_FULL + (items & 1)), hpad * 8);
-        ptx::bulk_load(base + ACC_SH + (items & 1) * ACC_HEADS * 8, src + ACC_COLS * hpad * 128, hpad * 8,
+        ptx::bulk_load(base + ACC_SH + (items & 1) * ACC_HEADS * 8, src + hpad * 2 * HEAD_DIM, hpad * 8,
                        bar(AB_H_FULL + (items & 1)));
         cols = 0;
         ++items;
         for (; cols < ACC_COLS; ++cols) {
           if (!wait(bar(AB_Q_EMPTY + cols), (items & 1))) { live = false; break; }
-          ptx::mbar_arrive_expect_tx(bar(AB_Q_FULL + cols), hpad * 128);
-          ptx::bulk_load(base + ACC_SQ + cols * col, src + cols * hpad * 128, hpad * 128, bar(AB_Q_FULL + cols));
+          const uint32_t bytes = cols < ACC_COLS - 1 ? hpad * 256 : hpad * 128;
+          ptx::mbar_arrive_expect_tx(bar(AB_Q_FULL + cols), bytes);
+          ptx::bulk_load(base + ACC_SQ + cols * col, src + cols * hpad * 256, bytes, bar(AB_Q_FULL + cols));
         }
         live = live && w.next_item(p);
       }
@@ -463,55 +524,58 @@ __global__ void __launch_bounds__(ACC_THREADS, 1) mla_accumulate_kernel(const __
     __syncwarp();
   } else if (warp >= ACC_EPI_WARP0) {
     // ------------------------------------------------------------------ epilogue
-    const int r = threadIdx.x - 32 * ACC_EPI_WARP0;      // the tile's key = tensor-memory lane
-    const uint32_t quad = static_cast<uint32_t>(warp - ACC_EPI_WARP0) << 21;
-    uint32_t tile = 0, items = 0;
+    const int r = threadIdx.x & 127;                     // the tile's key = tensor-memory lane
+    const uint32_t buf = (warp - ACC_EPI_WARP0) >> 2;    // this group's tiles: those of this parity
+    const uint32_t d = tbase + (static_cast<uint32_t>(warp & 3) << 21) + buf * 256;
+    uint32_t use = 0, items = 0;
     bool live = w.start(p, t0);
-    if (live && r == 0 && p.cache_lengths[w.b] > p.max_cache_length) raise_status(p.status, STATUS_BOUNDS);
-    AccKey key = live ? acc_key(p, w.b, w.item, w.j, r) : AccKey{0.f, 0.f, nullptr};
+    AccKey key{0.f, 0.f, nullptr}, nxt{0.f, 0.f, nullptr};
+    if (live && (w.j & 1) == static_cast<int>(buf)) key = acc_key(p, w.b, w.item, w.j, r);
     while (live) {
       const AccWalker cur = w;
-      live = w.next(p);
-      if (live && w.b != cur.b && r == 0 && p.cache_lengths[w.b] > p.max_cache_length)
+      const bool own = (cur.j & 1) == static_cast<int>(buf);
+      if (cur.item == 0 && cur.j == 0 && buf == 0 && r == 0 && p.cache_lengths[cur.b] > p.max_cache_length)
         raise_status(p.status, STATUS_BOUNDS);
-      // the next tile's scale and running sum are on their way while this tile is summed
-      const AccKey nxt = live ? acc_key(p, w.b, w.item, w.j, r) : AccKey{0.f, 0.f, nullptr};
+      if (cur.first_of_item() && !__all_sync(0xffffffffu, wait(bar(AB_H_FULL + (items & 1)), (items >> 1) & 1))) break;
+      live = w.next(p);
+      const bool next_own = live && (w.j & 1) == static_cast<int>(buf);
       const int i = static_cast<int>(p.divG.div(cur.item)), g = cur.item - i * p.G;
-      const uint32_t hpad = acc_hpad(p, g);
-      bool ok = !cur.first_of_item() || wait(bar(AB_H_FULL + (items & 1)), (items >> 1) & 1);
-      ok = ok && wait(bar(AB_ACC_FULL + (tile & 1)), (tile >> 1) & 1);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      ptx::tc_fence_after();
-      const uint32_t d = tbase + quad + (tile & 1) * 256, hf = base + ACC_SH + (items & 1) * ACC_HEADS * 8;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t h = 0;
-      for (; h + 32 <= hpad; h += 32) {
-        uint32_t hi[32], lo[32];
-        ptx::tmem_ld32(d + h, hi);
-        ptx::tmem_ld32(d + hpad + h, lo);
-        ptx::tmem_wait_ld();
-        acc_heads<32>(hi, lo, key.scale, hf + h * 8, sum);
+      const uint32_t hpad = acc_hpad(p, g), hf = base + ACC_SH + (items & 1) * ACC_HEADS * 8;
+      // the scale and running sum of this group's next tile are on their way while others are summed
+      if (next_own) nxt = acc_key(p, w.b, w.item, w.j, r);
+      if (own) {
+        if (!__all_sync(0xffffffffu, wait(bar(AB_ACC_FULL + buf), use & 1))) break;
+        ++use;
+        ptx::tc_fence_after();
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t h = 0;
+        for (; h + 32 <= hpad; h += 32) {
+          uint32_t hi[32], lo[32];
+          ptx::tmem_ld32(d + h, hi);
+          ptx::tmem_ld32(d + hpad + h, lo);
+          ptx::tmem_wait_ld();
+          acc_heads<32>(hi, lo, key.scale, hf + h * 8, sum);
+        }
+        for (; h < hpad; h += 8) {
+          uint32_t hi[8], lo[8];
+          tmem_ld8(d + h, hi);
+          tmem_ld8(d + hpad + h, lo);
+          ptx::tmem_wait_ld();
+          acc_heads<8>(hi, lo, key.scale, hf + h * 8, sum);
+        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(AB_ACC_EMPTY + buf));
+        if (key.dst) {
+          const uint32_t t = static_cast<uint32_t>(cur.j) * ACC_BN + r;
+          const float add = t <= acc_length(p, cur.b) + p.i0 + i ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
+          *key.dst = (cur.item == 0 && p.i0 == 0 ? key.base : *key.dst) + add;
+        }
       }
-      for (; h < hpad; h += 8) {
-        uint32_t hi[8], lo[8];
-        tmem_ld8(d + h, hi);
-        tmem_ld8(d + hpad + h, lo);
-        ptx::tmem_wait_ld();
-        acc_heads<8>(hi, lo, key.scale, hf + h * 8, sum);
-      }
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(bar(AB_ACC_EMPTY + (tile & 1)));
       if (cur.last_of_item()) {
         ptx::mbar_arrive(bar(AB_H_EMPTY + (items & 1)));
         ++items;
       }
-      if (key.dst) {
-        const uint32_t t = static_cast<uint32_t>(cur.j) * ACC_BN + r;
-        const float add = t <= acc_length(p, cur.b) + p.i0 + i ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
-        *key.dst = (cur.item == 0 && p.i0 == 0 ? key.base : *key.dst) + add;
-      }
-      key = nxt;
-      ++tile;
+      if (next_own) key = nxt;
     }
   }
   ptx::tc_fence_before();

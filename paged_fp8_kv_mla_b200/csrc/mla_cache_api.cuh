@@ -80,13 +80,14 @@ mla_status_t check_mha(const mla_paged_shape_t* s, uint32_t layer_idx, int32_t e
   return MLA_OK;
 }
 
-// blocks as {column bytes, rows, columns}: one box = `cols` columns of `box_rows` rows.
+// Rows of row_bytes at `blocks` as {column bytes, rows, all_cols columns}: one box = `cols` columns of
+// `box_rows` rows.
 mla_status_t make_row_map(CUtensorMap* map, const void* blocks, uint64_t rows, uint64_t row_bytes, int col_bytes,
-                          int box_rows, int cols) {
+                          int all_cols, int box_rows, int cols) {
   EncodeTiledFn enc = nullptr;
   const mla_status_t st = get_encode_fn(&enc);
   if (st != MLA_OK) return st;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(col_bytes), rows, row_bytes / col_bytes};
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(col_bytes), rows, static_cast<cuuint64_t>(all_cols)};
   const cuuint64_t strides[2] = {row_bytes, static_cast<cuuint64_t>(col_bytes)};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(col_bytes), static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(cols)};
   const cuuint32_t estr[3] = {1, 1, 1};
@@ -110,7 +111,7 @@ mla_status_t acc_plan(int64_t B, int64_t T, int64_t H, AccPlan* out) {
   AccPlan a{};
   const int64_t G = (H + mla::ACC_HEADS - 1) / mla::ACC_HEADS;
   a.heads = static_cast<uint32_t>(((H < mla::ACC_HEADS ? H : mla::ACC_HEADS) + 7) / 8 * 8);
-  a.item_bytes = a.heads * (mla::ACC_COLS * 128 + 8);
+  a.item_bytes = a.heads * (2 * mla::HEAD_DIM + 8);
   if (B * G > (1ll << 24)) return fail(MLA_ERR_UNSUPPORTED, "too many (request, head group) items");
   const int64_t token = B * G * a.item_bytes;
   int64_t tokens = (256ll << 20) / token;
@@ -245,7 +246,9 @@ mla_status_t mla_accumulate_weights_fp8(const void* q, const float* lse, const v
   if (st != MLA_OK) return st;
   mla::AccumulateParams p{};
   p.box_rows = gcd_int(d.P, mla::ACC_BN);
-  st = make_row_map(&p.tmap_k, blocks, rows, mla::HEAD_DIM, 64, p.box_rows, 1);
+  st = make_row_map(&p.tmap_k, blocks, rows, mla::HEAD_DIM, 128, 4, p.box_rows, 1);
+  if (st != MLA_OK) return st;
+  st = make_row_map(&p.tmap_r, static_cast<const char*>(blocks) + 512, rows, mla::HEAD_DIM, 64, 1, p.box_rows, 1);
   if (st != MLA_OK) return st;
   AccPlan plan{};
   st = acc_plan(d.B, d.T, d.H, &plan);
@@ -522,7 +525,8 @@ mla_status_t mla_mha_decode_paged(const void* q, const void* blocks, const float
   mla::MhaParams p{};
   const uint64_t rows = static_cast<uint64_t>(s->num_blocks) * s->kv_dim * s->num_layers * s->page_size;
   const int head_bytes = s->head_dim * element_bytes, col = head_bytes < 128 ? head_bytes : 128;
-  st = make_row_map(&p.tmap, blocks, rows, static_cast<uint64_t>(s->num_kv_heads) * head_bytes, col, m.box_rows,
+  st = make_row_map(&p.tmap, blocks, rows, static_cast<uint64_t>(s->num_kv_heads) * head_bytes, col,
+                    s->num_kv_heads * (head_bytes / col), m.box_rows,
                     m.hg * (head_bytes / col));
   if (st != MLA_OK) return st;
   p.q = static_cast<const uint16_t*>(q);
