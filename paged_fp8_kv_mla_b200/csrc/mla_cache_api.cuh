@@ -203,11 +203,19 @@ mla_status_t mha_launch(const mla::MhaParams& p, const MhaPlan& m, cudaStream_t 
   return MLA_OK;
 }
 
+// Lanes per token: as many as its 16-byte chunks in one plane, in powers of two up to a warp.
 template <int D, bool FP8>
 mla_status_t mha_store_launch(const mla::MhaStoreParams& p, cudaStream_t stream) {
-  const uint64_t per_cta = mla::MST_THREADS / (D / 8);
-  const uint64_t grid = (p.rows + per_cta - 1) / per_cta;
-  mla::mla_mha_store_kernel<D, FP8><<<dim3(static_cast<unsigned>(grid), 2), mla::MST_THREADS, 0, stream>>>(p);
+  const int lanes = p.chunks >= 32 ? 32 : p.chunks >= 16 ? 16 : 8;
+  const uint64_t grid = (static_cast<uint64_t>(p.tokens) * lanes + mla::MST_THREADS - 1) / mla::MST_THREADS;
+  if (grid * mla::MST_THREADS > 0xFFFFFFFFull) return fail(MLA_ERR_UNSUPPORTED, "too many new tokens (%u)", p.tokens);
+  const dim3 g(static_cast<unsigned>(grid), 2);
+  if (lanes == 32)
+    mla::mla_mha_store_kernel<D, FP8, 32><<<g, mla::MST_THREADS, 0, stream>>>(p);
+  else if (lanes == 16)
+    mla::mla_mha_store_kernel<D, FP8, 16><<<g, mla::MST_THREADS, 0, stream>>>(p);
+  else if (D == 64)
+    mla::mla_mha_store_kernel<64, FP8, 8><<<g, mla::MST_THREADS, 0, stream>>>(p);
   MLA_CUDA(cudaGetLastError());
   return MLA_OK;
 }
@@ -452,12 +460,13 @@ mla_status_t mla_mha_kv_store(const void* k, const void* v, const uint32_t* cach
   mla_status_t st = check_mha(s, layer_idx, element_bytes, blocks, scales, cache_lengths, lookup_table);
   if (st != MLA_OK) return st;
   mla::MhaStoreParams p{};
-  p.rows = static_cast<uint64_t>(s->batch) * num_new_tokens * s->num_kv_heads;
-  if (p.rows == 0) return MLA_OK;
+  const uint64_t tokens = static_cast<uint64_t>(s->batch) * num_new_tokens;
+  if (tokens == 0) return MLA_OK;
   if (!k || !v) return fail(MLA_ERR_INVALID_ARG, "k and v must be non-NULL");
   if (!aligned16(k) || !aligned16(v)) return fail(MLA_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
-  if (static_cast<uint64_t>(s->batch) * num_new_tokens >= (1ull << 31) || p.rows >= (1ull << 31))
-    return fail(MLA_ERR_UNSUPPORTED, "too many new rows (%llu)", p.rows);
+  if (tokens >= (1ull << 31)) return fail(MLA_ERR_UNSUPPORTED, "too many new tokens (%llu)", static_cast<unsigned long long>(tokens));
+  p.tokens = static_cast<unsigned int>(tokens);
+  p.chunks = s->num_kv_heads * s->head_dim / 8;
   p.k = static_cast<const uint16_t*>(k);
   p.v = static_cast<const uint16_t*>(v);
   p.cache_lengths = cache_lengths;
@@ -477,8 +486,8 @@ mla_status_t mla_mha_kv_store(const void* k, const void* v, const uint32_t* cach
   p.NB = s->num_blocks;
   p.NSB = s->num_scale_blocks;
   p.max_pages = s->max_pages;
-  p.divH = make_fastdiv(static_cast<uint32_t>(p.HKV));
   p.divT = make_fastdiv(num_new_tokens);
+  p.divP = make_fastdiv(static_cast<uint32_t>(p.P));
   if (s->head_dim == 64)
     return element_bytes == 1 ? mha_store_launch<64, true>(p, stream) : mha_store_launch<64, false>(p, stream);
   return element_bytes == 1 ? mha_store_launch<128, true>(p, stream) : mha_store_launch<128, false>(p, stream);

@@ -114,6 +114,75 @@ __device__ __forceinline__ void compact_walk(const CompactParams& p, const int32
   }
 }
 
+// The cache rows: a CTA moves one slice of SLICE bytes of every row, SLICE / 16 lanes per row, U rows per
+// lane and chunk.  The three dependent rounds of a chunk overlap with the chunks before it: while chunk n
+// waits for its barrier and is written, chunk n + 1's rows are on their way and chunk n + 2's pages are
+// looked up.  (Its rows may be read before chunk n is written: they lie at or above chunk n + 1.)
+template <int SLICE, int U>
+__device__ __forceinline__ void compact_rows(const CompactParams& p, const int32_t* kept, uint32_t m, const uint32_t* lut,
+                                             int plane, int slice) {
+  constexpr int LPR = SLICE / 16;                        // lanes per row
+  constexpr uint32_t ROWS = CMP_THREADS / LPR;           // rows of a chunk per step u
+  constexpr uint32_t CHUNK = ROWS * U;
+  constexpr uint32_t NONE = ~0u;
+  uint8_t* base = p.blocks + slice * SLICE + (threadIdx.x & (LPR - 1)) * 16;
+  const uint32_t j0 = threadIdx.x / LPR;
+  const uint32_t kv = static_cast<uint32_t>(plane) * p.NL + p.layer, pages = static_cast<uint32_t>(p.KVD) * p.NL;
+  // rows of a chunk: kept index and own index of each step; then pool rows (NONE: nothing to move)
+  auto indices = [&](uint32_t c0, uint32_t (&from)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t j = c0 + u * ROWS + j0;
+      from[u] = j < m ? static_cast<uint32_t>(kept[j]) : j;
+    }
+  };
+  auto rows = [&](uint32_t c0, const uint32_t (&from)[U], uint32_t (&src)[U], uint32_t (&dst)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t j = c0 + u * ROWS + j0, f = from[u];
+      src[u] = NONE;
+      dst[u] = NONE;
+      if (f == j) continue;                              // already in its place
+      const uint32_t fp = p.divP.div(f), tp = p.divP.div(j);
+      const bool in = f > j && fp < static_cast<uint32_t>(p.max_pages);
+      const uint32_t fb = in ? lut[fp] : NONE, tb = in ? lut[tp] : NONE;
+      if (fb < static_cast<uint32_t>(p.NB) && tb < static_cast<uint32_t>(p.NB)) {
+        src[u] = (fb * pages + kv) * p.P + (f - fp * p.P);   // below 2^31: the pool's rows are
+        dst[u] = (tb * pages + kv) * p.P + (j - tp * p.P);
+      } else {
+        raise_status(p.status, STATUS_BOUNDS);           // left as it is
+      }
+    }
+  };
+  uint32_t from[U], src[U], dst[U], next_dst[U];
+  uint4 v[U], next[U];
+  auto load = [&](uint4 (&to)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (src[u] != NONE) to[u] = ld_row(reinterpret_cast<const uint4*>(base + static_cast<size_t>(src[u]) * p.row_bytes));
+  };
+  indices(0, from);
+  rows(0, from, src, dst);
+  load(v);
+  indices(CHUNK, from);
+  rows(CHUNK, from, src, next_dst);
+  indices(2 * CHUNK, from);
+  for (uint32_t c0 = 0; c0 < m; c0 += CHUNK) {
+    load(next);                                          // chunk n + 1
+    __syncthreads();                                     // chunk n has been read by every thread
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (dst[u] != NONE) *reinterpret_cast<uint4*>(base + static_cast<size_t>(dst[u]) * p.row_bytes) = v[u];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      v[u] = next[u];
+      dst[u] = next_dst[u];
+    }
+    rows(c0 + 2 * CHUNK, from, src, next_dst);
+    indices(c0 + 3 * CHUNK, from);
+  }
+}
+
 // grid (kv planes * slices + kv planes (scales) + 1 (accumulated weights), requests)
 template <int SLICE>
 __global__ void __launch_bounds__(CMP_THREADS, 2) mla_compact_kernel(const __grid_constant__ CompactParams p) {
@@ -128,9 +197,7 @@ __global__ void __launch_bounds__(CMP_THREADS, 2) mla_compact_kernel(const __gri
   int i = blockIdx.x;
   if (i < p.KVD * p.slices) {
     const int plane = i / p.slices, slice = i - plane * p.slices;
-    const CompactColumn<uint4> col{reinterpret_cast<uint4*>(p.blocks) + slice * (SLICE / 16), p.row_bytes / 16, lut,
-                                   static_cast<uint32_t>(p.NB), static_cast<uint32_t>(plane), ~0u};
-    compact_walk<uint4, 4>(p, kept, m, SLICE / 16, [](uint32_t e) { return e / (SLICE / 16); }, col);
+    compact_rows<SLICE, 4>(p, kept, m, lut, plane, slice);
     return;
   }
   i -= p.KVD * p.slices;
