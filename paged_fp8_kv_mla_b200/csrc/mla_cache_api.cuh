@@ -27,10 +27,14 @@ mla_status_t cache_device(int* sms) {
     };
     MLA_CUDA(smem(mla::mla_accumulate_kernel, mla::ACC_SMEM_ALLOC));
     MLA_CUDA(smem(mla::mla_select_kernel, mla::SEL_KEYS_OFF + mla::SEL_CACHE * 4));
-    MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, false>, mla::MHA_SMEM_LIMIT));
-    MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, true>, mla::MHA_SMEM_LIMIT));
-    MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, false>, mla::MHA_SMEM_LIMIT));
-    MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, true>, mla::MHA_SMEM_LIMIT));
+    MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, false, 1>, mla::MHA_SMEM_LIMIT));
+    MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, false, 2>, mla::MHA_SMEM_LIMIT));
+    MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, true, 1>, mla::MHA_SMEM_LIMIT));
+    MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, true, 2>, mla::MHA_SMEM_LIMIT));
+    MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, false, 1>, mla::MHA_SMEM_LIMIT));
+    MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, false, 2>, mla::MHA_SMEM_LIMIT));
+    MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, true, 1>, mla::MHA_SMEM_LIMIT));
+    MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, true, 2>, mla::MHA_SMEM_LIMIT));
     g_sms[dev] = n;
   }
   *sms = g_sms[dev];
@@ -124,7 +128,7 @@ mla_status_t acc_plan(int64_t B, int64_t T, int64_t H, AccPlan* out) {
 
 // How a multi-head decode is laid out (the rules the kernel's header comment describes).
 struct MhaPlan {
-  int R, hg, mt, kw, head_groups, row_groups, tile, box_rows, stages, NC, one_item;
+  int R, hg, mt, kw, ks, head_groups, row_groups, tile, box_rows, stages, NC, one_item;
   uint32_t plane_bytes, stage_bytes, smem;
   uint64_t part_lse_off, desc_off, total;
 };
@@ -154,9 +158,11 @@ mla_status_t mha_plan(const mla_paged_shape_t* s, uint32_t T, uint32_t max_cache
   m.hg = (s->num_kv_heads + m.head_groups - 1) / m.head_groups;
   m.kw = 1;
   while (2 * m.kw * m.hg * m.mt <= mla::MHA_WARPS) m.kw *= 2;
-  // Tile: 16 keys per warp, doubled while a ring stage stays within 32 KB.
+  // Tile: 32 keys per warp at a time where a run of pages holds them and a ring stage of them takes at most
+  // 72 KB (three stages), else 16; doubled while a stage stays within 32 KB.
   const uint32_t per_key = 2u * m.hg * s->head_dim * element_bytes + (element_bytes == 1 ? 8u * s->num_kv_heads : 0u);
-  m.tile = 16 * m.kw;
+  m.ks = s->page_size % 32 == 0 && 32 * m.kw * per_key <= 73728 ? 2 : 1;
+  m.tile = 16 * m.ks * m.kw;
   while (m.tile < 128 && 2 * m.tile * per_key <= 32768) m.tile *= 2;
   m.box_rows = gcd_int(s->page_size, m.tile);
   m.plane_bytes = static_cast<uint32_t>(m.tile) * m.hg * s->head_dim * element_bytes;
@@ -187,7 +193,10 @@ mla_status_t mha_plan(const mla_paged_shape_t* s, uint32_t T, uint32_t max_cache
 
 template <int D, bool FP8>
 mla_status_t mha_launch(const mla::MhaParams& p, const MhaPlan& m, cudaStream_t stream) {
-  mla::mla_mha_decode_kernel<D, FP8><<<m.NC, mla::MHA_THREADS, m.smem, stream>>>(p);
+  if (m.ks == 2)
+    mla::mla_mha_decode_kernel<D, FP8, 2><<<m.NC, mla::MHA_THREADS, m.smem, stream>>>(p);
+  else
+    mla::mla_mha_decode_kernel<D, FP8, 1><<<m.NC, mla::MHA_THREADS, m.smem, stream>>>(p);
   MLA_CUDA(cudaGetLastError());
   if (m.one_item) return MLA_OK;
   cudaLaunchConfig_t cfg = {};

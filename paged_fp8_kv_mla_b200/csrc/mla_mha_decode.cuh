@@ -215,65 +215,82 @@ struct MhaRows {
     vref = 0.f;
   }
 
-  // 16 keys: key0 + 0..15 at rows row .. row + 15 of a run; n: the request's stored keys.
+  // 16 KS keys from key0 on, at rows row .. of a run; n: the request's stored keys.  KS = 2 halves the
+  // rescales and reductions per key and gives the MMAs four independent accumulators instead of two.
+  template <int KS>
   __device__ __forceinline__ void step(const MhaParams& p, uint32_t krun, uint32_t vrun, int rows, int row, int col,
                                        uint32_t ks, uint32_t vs, uint32_t key0, uint32_t n, int lane) {
     const int t = lane & 3;
-    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    float s[2 * KS][4];                 // [8-key group][rows g: keys 2t, 2t + 1; rows g + 8: the same]
+#pragma unroll
+    for (int x = 0; x < 2 * KS; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) s[x][y] = 0.f;
     {
       const uint32_t r = row + (lane & 7) + ((lane >> 4) << 3);
       const uint32_t half = ((lane >> 3) & 1) * 16;
       if (!FP8) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t kb[4];
-          ldsm4(at(krun, rows, col + k * 32 / CW, r, (k * 32) % CW + half), kb);
-          mma_16816_bf16(s[0], qa[k], kb[0], kb[1]);
-          mma_16816_bf16(s[1], qa[k], kb[2], kb[3]);
-        }
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int y = 0; y < KS; ++y) {
+            uint32_t kb[4];
+            ldsm4(at(krun, rows, col + k * 32 / CW, r + 16 * y, (k * 32) % CW + half), kb);
+            mma_16816_bf16(s[2 * y], qa[k], kb[0], kb[1]);
+            mma_16816_bf16(s[2 * y + 1], qa[k], kb[2], kb[3]);
+          }
       } else {
 #pragma unroll
-        for (int k = 0; k < D / 16; k += 2) {
-          uint32_t kb[4];
-          ldsm4(at(krun, rows, col, r, k * 16 + half), kb);
+        for (int k = 0; k < D / 16; k += 2)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)   // x & 1: k step, x >> 1: key half
-            mma_16816_f16(s[x >> 1], qa[k + (x & 1)], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[x])),
-                          ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[x] >> 16)));
+          for (int y = 0; y < KS; ++y) {
+            uint32_t kb[4];
+            ldsm4(at(krun, rows, col, r + 16 * y, k * 16 + half), kb);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)   // x & 1: k step, x >> 1: key half
+              mma_16816_f16(s[2 * y + (x >> 1)], qa[k + (x & 1)], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[x])),
+                            ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[x] >> 16)));
+          }
+      }
+    }
+    float sv[2 * KS][2];
+#pragma unroll
+    for (int x = 0; x < 2 * KS; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {     // key 8 x + 2 t + y
+        float f = 1.f;
+        if (FP8) {
+          f = ptx::ld_shared_f32(ks + (8 * x + 2 * t + y) * p.HKV * 4);
+          sv[x][y] = ptx::ld_shared_f32(vs + (8 * x + 2 * t + y) * p.HKV * 4);
         }
+        s[x][y] *= FP8 ? xs[0] * f : xs[0];
+        s[x][y + 2] *= FP8 ? xs[1] * f : xs[1];
       }
-    }
-    float sv[4] = {1.f, 1.f, 1.f, 1.f};
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {       // keys 2t, 2t + 1, 2t + 8, 2t + 9
-      const uint32_t key = 2 * t + (x & 1) + (x >> 1) * 8;
-      float f = 1.f;
-      if (FP8) {
-        f = ptx::ld_shared_f32(ks + key * p.HKV * 4);
-        sv[x] = ptx::ld_shared_f32(vs + key * p.HKV * 4);
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float& y = s[x >> 1][(x & 1) + 2 * u];
-        y *= FP8 ? xs[u] * f : xs[u];
-      }
-    }
-    const bool edge = key0 + 15 > n - p.T;   // some row may not see some of the keys
+    const bool edge = key0 + 16 * KS - 1 > n - p.T;   // some row may not see some of the keys
     if (edge) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint32_t key = key0 + 2 * t + (x & 1) + (x >> 1) * 8;
-        if (key > last[0]) s[x >> 1][x & 1] = -INFINITY;
-        if (key > last[1]) s[x >> 1][(x & 1) + 2] = -INFINITY;
-        if (FP8 && key >= n) sv[x] = 0.f;
-      }
+      for (int x = 0; x < 2 * KS; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t key = key0 + 8 * x + 2 * t + y;
+          if (key > last[0]) s[x][y] = -INFINITY;
+          if (key > last[1]) s[x][y + 2] = -INFINITY;
+          if (FP8 && key >= n) sv[x][y] = 0.f;
+        }
     }
     // running maxima; a row that has seen no key yet keeps reference 0
-    const float m0 = fmaxf(m[0], quad_max(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]))));
-    const float m1 = fmaxf(m[1], quad_max(fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]))));
+    float m0 = s[0][0], m1 = s[0][2], top = 0.f;
+#pragma unroll
+    for (int x = 0; x < 2 * KS; ++x) {
+      m0 = fmaxf(m0, fmaxf(s[x][0], s[x][1]));
+      m1 = fmaxf(m1, fmaxf(s[x][2], s[x][3]));
+      if (FP8) top = fmaxf(top, fmaxf(fabsf(sv[x][0]), fabsf(sv[x][1])));
+    }
+    m0 = fmaxf(m[0], quad_max(m0));
+    m1 = fmaxf(m[1], quad_max(m1));
     float ref = vref;
     if (FP8) {
-      const float top = quad_max(fmaxf(fmaxf(fabsf(sv[0]), fabsf(sv[1])), fmaxf(fabsf(sv[2]), fabsf(sv[3]))));
+      top = quad_max(top);
       if (top > vref) ref = pow2(min(max(static_cast<int>(__float_as_uint(top) >> 23) - 126, -126), 126));
     }
     const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
@@ -295,56 +312,63 @@ struct MhaRows {
     }
     // 1 / vref: a power of two's reciprocal has the mirrored exponent
     const float inv = FP8 && vref > 0.f ? __uint_as_float(0x7F000000u - __float_as_uint(vref)) : 0.f;
-    uint32_t pa[4];
+    uint32_t pa[KS][4];
 #pragma unroll
-    for (int x = 0; x < 4; x += 2) {
-      const int c = x >> 1;
-      const float p00 = ptx::ex2_approx(s[c][0] - r0), p01 = ptx::ex2_approx(s[c][1] - r0);
-      const float p10 = ptx::ex2_approx(s[c][2] - r1), p11 = ptx::ex2_approx(s[c][3] - r1);
+    for (int x = 0; x < 2 * KS; ++x) {
+      const float p00 = ptx::ex2_approx(s[x][0] - r0), p01 = ptx::ex2_approx(s[x][1] - r0);
+      const float p10 = ptx::ex2_approx(s[x][2] - r1), p11 = ptx::ex2_approx(s[x][3] - r1);
       l[0] += p00 + p01;
       l[1] += p10 + p11;
+      uint32_t* a = &pa[x >> 1][(x & 1) * 2];
       if (FP8) {
-        const float w0 = sv[x] * inv, w1 = sv[x + 1] * inv;
-        pa[x] = ptx::pack_f16x2(p00 * w0, p01 * w1);
-        pa[x + 1] = ptx::pack_f16x2(p10 * w0, p11 * w1);
+        const float w0 = sv[x][0] * inv, w1 = sv[x][1] * inv;
+        a[0] = ptx::pack_f16x2(p00 * w0, p01 * w1);
+        a[1] = ptx::pack_f16x2(p10 * w0, p11 * w1);
       } else {
-        pa[x] = ptx::pack_bf16x2(p00, p01);
-        pa[x + 1] = ptx::pack_bf16x2(p10, p11);
+        a[0] = ptx::pack_bf16x2(p00, p01);
+        a[1] = ptx::pack_bf16x2(p10, p11);
       }
     }
     // Rows of the cache past the request's end hold anything: their values are zeroed, since a weight of
     // 0 does not silence an infinity.  keep: the two keys of a register that exist.
-    const bool tail = key0 + 16 > n;
-    uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;
-    if (tail) {
-      const uint32_t k0 = key0 + 2 * t, k1 = k0 + 8;
-      keep0 = (k0 < n ? 0xFFFFu : 0u) | (k0 + 1 < n ? 0xFFFF0000u : 0u);
-      keep1 = (k1 < n ? 0xFFFFu : 0u) | (k1 + 1 < n ? 0xFFFF0000u : 0u);
+    uint32_t keep[2 * KS];
+#pragma unroll
+    for (int x = 0; x < 2 * KS; ++x) keep[x] = 0xFFFFFFFFu;
+    if (key0 + 16 * KS > n) {
+#pragma unroll
+      for (int x = 0; x < 2 * KS; ++x) {
+        const uint32_t k0 = key0 + 8 * x + 2 * t;
+        keep[x] = (k0 < n ? 0xFFFFu : 0u) | (k0 + 1 < n ? 0xFFFF0000u : 0u);
+      }
     }
     const uint32_t r = row + (lane & 7) + ((lane >> 3) & 1) * 8;
     const uint32_t half = (lane >> 4) * 16;
     if (!FP8) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        uint32_t vb[4];
-        ldsm4_t(at(vrun, rows, col + k * 32 / CW, r, (k * 32) % CW + half), vb);
-        mma_16816_bf16(o[2 * k], pa, vb[0] & keep0, vb[1] & keep1);
-        mma_16816_bf16(o[2 * k + 1], pa, vb[2] & keep0, vb[3] & keep1);
-      }
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int y = 0; y < KS; ++y) {
+          uint32_t vb[4];
+          ldsm4_t(at(vrun, rows, col + k * 32 / CW, r + 16 * y, (k * 32) % CW + half), vb);
+          mma_16816_bf16(o[2 * k], pa[y], vb[0] & keep[2 * y], vb[1] & keep[2 * y + 1]);
+          mma_16816_bf16(o[2 * k + 1], pa[y], vb[2] & keep[2 * y], vb[3] & keep[2 * y + 1]);
+        }
     } else {
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {        // 32 dims: two blocks of 16, an even and an odd tile each
-        uint32_t vb[4];
-        ldsm4_t(at(vrun, rows, col, r, k * 32 + half), vb);
+      for (int k = 0; k < D / 32; ++k)          // 32 dims: two blocks of 16, an even and an odd tile each
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t a = vb[2 * x] & keep0, b = vb[2 * x + 1] & keep1;
-          mma_16816_f16(o[4 * k + 2 * x], pa, ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(a, 0, 0x4420))),
-                        ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(b, 0, 0x4420))));
-          mma_16816_f16(o[4 * k + 2 * x + 1], pa, ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(a, 0, 0x4431))),
-                        ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(b, 0, 0x4431))));
+        for (int y = 0; y < KS; ++y) {
+          uint32_t vb[4];
+          ldsm4_t(at(vrun, rows, col, r + 16 * y, k * 32 + half), vb);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t a = vb[2 * x] & keep[2 * y], b = vb[2 * x + 1] & keep[2 * y + 1];
+            mma_16816_f16(o[4 * k + 2 * x], pa[y], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(a, 0, 0x4420))),
+                          ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(b, 0, 0x4420))));
+            mma_16816_f16(o[4 * k + 2 * x + 1], pa[y], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(a, 0, 0x4431))),
+                          ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(b, 0, 0x4431))));
+          }
         }
-      }
     }
   }
 
@@ -392,7 +416,7 @@ struct MhaRows {
   }
 };
 
-template <int D, bool FP8>
+template <int D, bool FP8, int KS>
 __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __grid_constant__ MhaParams p) {
   using Rows = MhaRows<D, FP8>;
   constexpr int CPH = D * (FP8 ? 1 : 2) / Rows::CW;      // columns per head
@@ -546,13 +570,13 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
         const uint32_t kst = base + s * p.stage_bytes, vst = kst + p.plane_bytes;
         const uint32_t sst = vst + p.plane_bytes;
         const uint32_t box_bytes = p.hg * CPH * p.box_rows * Rows::CW;
-        for (int g = kp * 16; work && g < p.tile; g += p.kw * 16) {
+        for (int g = kp * 16 * KS; work && g < p.tile; g += p.kw * 16 * KS) {
           const uint32_t key0 = static_cast<uint32_t>(j) * p.tile + g;
           if (key0 >= stored) break;
           const int run = g / p.box_rows, row = g - run * p.box_rows;
           if ((bad >> run) & 1u) continue;               // no such page: its keys are left out
           const uint32_t ks = sst + (g * p.HKV + kvh) * 4;
-          w.step(p, kst + run * box_bytes, vst + run * box_bytes, p.box_rows, row, hl * CPH, ks,
+          w.template step<KS>(p, kst + run * box_bytes, vst + run * box_bytes, p.box_rows, row, hl * CPH, ks,
                  ks + p.tile * p.HKV * 4, key0, stored, lane);
         }
         __syncwarp();
