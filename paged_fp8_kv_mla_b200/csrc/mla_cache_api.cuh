@@ -586,6 +586,7 @@ mla_status_t mla_mha_decode_paged(const void* q, const void* blocks, const float
   p.row_groups = m.row_groups;
   p.tile = m.tile;
   p.box_rows = m.box_rows;
+  while ((1 << p.box_shift) < m.box_rows) ++p.box_shift;
   p.stages = m.stages;
   p.plane_bytes = m.plane_bytes;
   p.stage_bytes = m.stage_bytes;

@@ -39,7 +39,7 @@
 namespace mla {
 
 constexpr int MHA_WARPS = 8;                      // consumer warps
-constexpr int MHA_THREADS = 32 * (MHA_WARPS + 1);
+constexpr int MHA_THREADS = 32 * (MHA_WARPS + 4);   // consumers, and a warpgroup for the producer warp
 constexpr int MHA_ROWS = 16 * MHA_WARPS;          // rows of a CTA at most
 constexpr int MHA_MAX_STAGES = 8;
 constexpr int MHA_MAX_RUNS = 16;                  // page runs of a tile
@@ -63,7 +63,7 @@ struct MhaParams {
   unsigned int max_cache_length;
   int hg, mt, kw;                  // kv heads per CTA, row tiles per CTA, warps over the keys of a tile
   int head_groups, row_groups;     // of a request: its items
-  int tile, box_rows, stages;      // keys per tile, keys per box, ring depth
+  int tile, box_rows, box_shift, stages;   // keys per tile, keys per box (a power of two) and its log2, ring depth
   uint32_t plane_bytes, stage_bytes;   // of a tile's K (or V); of a ring stage
   int one_item;                    // 1: CTA c computes item c alone
   FastDiv divP, divG;              // by the page size and by G = H / HKV
@@ -78,6 +78,16 @@ __device__ __forceinline__ void mma_16816_bf16(float (&c)[4], const uint32_t (&a
 __device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_16816_bf16(float2 (&c)[2], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0].x), "+f"(c[0].y), "+f"(c[1].x), "+f"(c[1].y)
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_16816_f16(float2 (&c)[2], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0].x), "+f"(c[0].y), "+f"(c[1].x), "+f"(c[1].y)
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -102,6 +112,9 @@ __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t nthreads, bool v) 
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float warp_max(float v) {   // v >= 0
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 __device__ __forceinline__ float quad_sum(float v) {
   v += __shfl_xor_sync(0xffffffffu, v, 1);
@@ -145,7 +158,7 @@ struct MhaWalker {
 // Shared memory after the ring: the warps' merge buffers (kw > 1), then the barriers.
 template <int D>
 __host__ __device__ constexpr uint32_t mha_merge_bytes() { return (MHA_WARPS / 2) * 16 * (D + 2) * 4; }
-constexpr uint32_t MHA_MISC_BYTES = 8 * 2 * MHA_MAX_STAGES + 4 * MHA_MAX_STAGES + 64 + 8 * (MHA_WARPS + 1) + 64;
+constexpr uint32_t MHA_MISC_BYTES = 8 * 4 * MHA_MAX_STAGES + 4 * MHA_MAX_STAGES + 64 + 8 * (MHA_WARPS + 4) + 64;
 
 // One warp's state: 16 rows (thread: rows lane / 4 and lane / 4 + 8) of one kv head.
 template <int D, bool FP8>
@@ -153,19 +166,20 @@ struct MhaRows {
   static constexpr int CW = D * (FP8 ? 1 : 2) < 128 ? D * (FP8 ? 1 : 2) : 128;   // bytes of a column
   uint32_t qa[D / 16][4];          // q as A fragments (bf16, or f16 times a power of two per row)
   float o[D / 8][4];
-  float m[2], l[2];                // running maximum (base 2) and this thread's part of the sum
-  float xs[2];                     // score factor of the thread's two rows
+  float m[2];                      // reference maximum (base 2) of the thread's two rows
+  float2 l[2];                     // this thread's part of the sum (even, odd keys)
+  float xs;                        // score factor
+  uint32_t koff, voff;             // this lane's place in a 16-key block of K and V
   uint32_t last[2];                // last visible key of each row
   float vref;                      // e4m3: power-of-two bound of V's scales so far (0: none yet)
 
-  // byte `o` of key row `r` of the CTA's column `col` in a run of `rows` keys at `run`
-  static __device__ __forceinline__ uint32_t at(uint32_t run, int rows, int col, uint32_t r, uint32_t o) {
-    const uint32_t sw = CW == 128 ? (r & 7u) << 4 : ((r >> 1) & 3u) << 4;
-    return run + (col * rows + r) * CW + (o ^ sw);
-  }
+  static __device__ __forceinline__ uint32_t swizzle(uint32_t r) { return CW == 128 ? (r & 7u) << 4 : ((r >> 1) & 3u) << 4; }
 
+  // Query rows row0 .. row0 + 15 of kv head kvh (rows past the last one are zero).  For e4m3 caches q is
+  // brought to f16 by one power of two for the 16 rows (largest value into [2^12, 2^13)).
   __device__ __forceinline__ void load_q(const MhaParams& p, int b, int kvh, int row0, int lane) {
     const int t = lane & 3;
+    uint32_t m2 = 0;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int r = row0 + (lane >> 2) + 8 * u;
@@ -174,131 +188,138 @@ struct MhaRows {
       const int h = kvh * p.divG.d + (r - i * p.divG.d);
       last[u] = mha_length(p, b) + i;
       const uint16_t* src = p.q + ((static_cast<size_t>(b) * p.T + i) * p.H + h) * D;
-      if (!FP8) {
-        xs[u] = p.scale_log2;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
+      for (int k = 0; k < D / 16; ++k) {
+        if (!FP8) {
           qa[k][u] = have ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * t) : 0u;
           qa[k][u + 2] = have ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8 + 2 * t) : 0u;
-        }
-      } else {
-        uint32_t m2 = 0;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
+        } else {
           const uint2 v = have ? *reinterpret_cast<const uint2*>(src + 16 * k + 4 * t) : make_uint2(0, 0);
           qa[k][u] = v.x;
           qa[k][u + 2] = v.y;
           m2 = __vmaxu2(__vmaxu2(m2, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
         }
-        m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
-        m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 2));
-        const uint32_t big = max(m2 & 0xFFFFu, m2 >> 16);
-        // largest value into [2^12, 2^13); as two factors, since the power can be 2^126
-        const int e = big == 0 ? 0 : min(max(12 - (static_cast<int>(big >> 7) - 127), -115), 126);
-        const float f1 = pow2(e >> 1), f2 = pow2(e - (e >> 1));
-        xs[u] = big >= 0x7F80u ? __uint_as_float(0x7FC00000u) : p.scale_log2 * pow2(-(e >> 1)) * pow2(-(e - (e >> 1)));
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-          for (int x = 0; x < 4; x += 2) {
-            const uint32_t w = qa[k][u + x];
-            qa[k][u + x] = ptx::pack_f16x2(__uint_as_float(w << 16) * f1 * f2, __uint_as_float(w & 0xFFFF0000u) * f1 * f2);
-          }
       }
       m[u] = -INFINITY;
-      l[u] = 0.f;
+      l[u] = make_float2(0.f, 0.f);
+    }
+    xs = p.scale_log2;
+    if (FP8) {
+      const uint32_t big = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+      const int e = big == 0 ? 0 : min(max(12 - (static_cast<int>(big >> 7) - 127), -115), 126);
+      const float f = pow2(e);
+      xs = big >= 0x7F80u ? __uint_as_float(0x7FC00000u) : p.scale_log2 * pow2(-e);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          qa[k][x] = ptx::pack_f16x2(__uint_as_float(qa[k][x] << 16) * f, __uint_as_float(qa[k][x] & 0xFFFF0000u) * f);
     }
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
 #pragma unroll
       for (int x = 0; x < 4; ++x) o[n][x] = 0.f;
     vref = 0.f;
+    // ldmatrix rows and 16-byte units of this lane: K by keys (lane & 7) + 8 (lane / 16), V by keys lane & 15;
+    // a row's swizzle depends on the key's low bits only, which a step's multiple of 16 does not change
+    const uint32_t kr = (lane & 7) + ((lane >> 4) << 3), vr = lane & 15;
+    koff = kr * CW + ((((lane >> 3) & 1) * 16) ^ swizzle(kr));
+    voff = vr * CW + (((lane >> 4) * 16) ^ swizzle(vr));
   }
 
-  // 16 KS keys from key0 on, at rows row .. of a run; n: the request's stored keys.  KS = 2 halves the
-  // rescales and reductions per key and gives the MMAs four independent accumulators instead of two.
+  // A step takes 16 KS keys, at rows row .. of a page run.  KS = 2 halves the rescales and reductions per
+  // key and gives the MMAs four independent accumulators instead of two.
+  // Products q K^T: s[8-key group][row lane / 4: keys 2t, 2t + 1; row lane / 4 + 8: the same], t = lane % 4.
+  // kcol: the head's first column at the step's first row; pitch: bytes from column to column.
   template <int KS>
-  __device__ __forceinline__ void step(const MhaParams& p, uint32_t krun, uint32_t vrun, int rows, int row, int col,
-                                       uint32_t ks, uint32_t vs, uint32_t key0, uint32_t n, int lane) {
+  __device__ __forceinline__ void scores(uint32_t kcol, uint32_t pitch, float2 (&s)[2 * KS][2]) const {
+#pragma unroll
+    for (int x = 0; x < 2 * KS; ++x) s[x][0] = s[x][1] = make_float2(0.f, 0.f);
+    const uint32_t a0 = kcol + koff, a1 = a0 + pitch;
+    if (!FP8) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int y = 0; y < KS; ++y) {
+          uint32_t kb[4];
+          ldsm4(((k * 32 < CW ? a0 : a1) ^ ((k * 32) % CW)) + y * 16 * CW, kb);
+          mma_16816_bf16(s[2 * y], qa[k], kb[0], kb[1]);
+          mma_16816_bf16(s[2 * y + 1], qa[k], kb[2], kb[3]);
+        }
+    } else {
+#pragma unroll
+      for (int k = 0; k < D / 16; k += 2)
+#pragma unroll
+        for (int y = 0; y < KS; ++y) {
+          uint32_t kb[4];
+          ldsm4((a0 ^ (k * 16)) + y * 16 * CW, kb);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)   // x & 1: k step, x >> 1: key half
+            mma_16816_f16(s[2 * y + (x >> 1)], qa[k + (x & 1)], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[x])),
+                          ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[x] >> 16)));
+        }
+    }
+  }
+
+  // Scores to weights (pa: A fragments of the value product) against a reference maximum that trails the
+  // running one by at most LAZY (log2): weights stay below 2^LAZY and O is rescaled rarely.  ks, vs: the
+  // scales of the step's first key, sstep bytes from key to key; key0: the first key, n: stored keys.
+  static constexpr float LAZY = 6.f;
+  template <int KS>
+  __device__ __forceinline__ void weights(const MhaParams& p, float2 (&s)[2 * KS][2], uint32_t ks, uint32_t vs, uint32_t sstep,
+                                          uint32_t key0, uint32_t n, int lane, uint32_t (&pa)[KS][4]) {
     const int t = lane & 3;
-    float s[2 * KS][4];                 // [8-key group][rows g: keys 2t, 2t + 1; rows g + 8: the same]
+    float2 sv[2 * KS];
+    if (FP8) {
+      ks += 2 * t * sstep;
+      vs += 2 * t * sstep;
+    }
 #pragma unroll
-    for (int x = 0; x < 2 * KS; ++x)
+    for (int x = 0; x < 2 * KS; ++x) {  // keys 8 x + 2 t, + 1
+      float2 f = make_float2(xs, xs);
+      if (FP8) {
+        f = __fmul2_rn(make_float2(ptx::ld_shared_f32(ks), ptx::ld_shared_f32(ks + sstep)), f);
+        sv[x] = make_float2(ptx::ld_shared_f32(vs), ptx::ld_shared_f32(vs + sstep));
+        ks += 8 * sstep;
+        vs += 8 * sstep;
+      }
+      s[x][0] = __fmul2_rn(s[x][0], f);
+      s[x][1] = __fmul2_rn(s[x][1], f);
+    }
+    if (key0 + 16 * KS - 1 > n - p.T) {   // some row may not see some of the keys
 #pragma unroll
-      for (int y = 0; y < 4; ++y) s[x][y] = 0.f;
-    {
-      const uint32_t r = row + (lane & 7) + ((lane >> 4) << 3);
-      const uint32_t half = ((lane >> 3) & 1) * 16;
-      if (!FP8) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-          for (int y = 0; y < KS; ++y) {
-            uint32_t kb[4];
-            ldsm4(at(krun, rows, col + k * 32 / CW, r + 16 * y, (k * 32) % CW + half), kb);
-            mma_16816_bf16(s[2 * y], qa[k], kb[0], kb[1]);
-            mma_16816_bf16(s[2 * y + 1], qa[k], kb[2], kb[3]);
-          }
-      } else {
-#pragma unroll
-        for (int k = 0; k < D / 16; k += 2)
-#pragma unroll
-          for (int y = 0; y < KS; ++y) {
-            uint32_t kb[4];
-            ldsm4(at(krun, rows, col, r + 16 * y, k * 16 + half), kb);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)   // x & 1: k step, x >> 1: key half
-              mma_16816_f16(s[2 * y + (x >> 1)], qa[k + (x & 1)], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[x])),
-                            ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[x] >> 16)));
-          }
+      for (int x = 0; x < 2 * KS; ++x) {
+        const uint32_t key = key0 + 8 * x + 2 * t;
+        if (key > last[0]) s[x][0].x = -INFINITY;
+        if (key + 1 > last[0]) s[x][0].y = -INFINITY;
+        if (key > last[1]) s[x][1].x = -INFINITY;
+        if (key + 1 > last[1]) s[x][1].y = -INFINITY;
+        if (FP8 && key >= n) sv[x].x = 0.f;
+        if (FP8 && key + 1 >= n) sv[x].y = 0.f;
       }
     }
-    float sv[2 * KS][2];
-#pragma unroll
-    for (int x = 0; x < 2 * KS; ++x)
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {     // key 8 x + 2 t + y
-        float f = 1.f;
-        if (FP8) {
-          f = ptx::ld_shared_f32(ks + (8 * x + 2 * t + y) * p.HKV * 4);
-          sv[x][y] = ptx::ld_shared_f32(vs + (8 * x + 2 * t + y) * p.HKV * 4);
-        }
-        s[x][y] *= FP8 ? xs[0] * f : xs[0];
-        s[x][y + 2] *= FP8 ? xs[1] * f : xs[1];
-      }
-    const bool edge = key0 + 16 * KS - 1 > n - p.T;   // some row may not see some of the keys
-    if (edge) {
-#pragma unroll
-      for (int x = 0; x < 2 * KS; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t key = key0 + 8 * x + 2 * t + y;
-          if (key > last[0]) s[x][y] = -INFINITY;
-          if (key > last[1]) s[x][y + 2] = -INFINITY;
-          if (FP8 && key >= n) sv[x][y] = 0.f;
-        }
-    }
-    // running maxima; a row that has seen no key yet keeps reference 0
-    float m0 = s[0][0], m1 = s[0][2], top = 0.f;
+    float m0 = s[0][0].x, m1 = s[0][1].x, top = 0.f;
 #pragma unroll
     for (int x = 0; x < 2 * KS; ++x) {
-      m0 = fmaxf(m0, fmaxf(s[x][0], s[x][1]));
-      m1 = fmaxf(m1, fmaxf(s[x][2], s[x][3]));
-      if (FP8) top = fmaxf(top, fmaxf(fabsf(sv[x][0]), fabsf(sv[x][1])));
+      m0 = fmaxf(m0, fmaxf(s[x][0].x, s[x][0].y));
+      m1 = fmaxf(m1, fmaxf(s[x][1].x, s[x][1].y));
+      if (FP8) top = fmaxf(top, fmaxf(fabsf(sv[x].x), fabsf(sv[x].y)));
     }
-    m0 = fmaxf(m[0], quad_max(m0));
-    m1 = fmaxf(m[1], quad_max(m1));
-    float ref = vref;
-    if (FP8) {
-      top = quad_max(top);
-      if (top > vref) ref = pow2(min(max(static_cast<int>(__float_as_uint(top) >> 23) - 126, -126), 126));
-    }
-    const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
-    if (__any_sync(0xffffffffu, m0 != m[0] || m1 != m[1] || ref != vref)) {
-      const float c0 = ptx::ex2_approx(m[0] - r0), c1 = ptx::ex2_approx(m[1] - r1);   // ex2(-inf) = 0
+    // (the row's own lanes may disagree on whether a rescale is due: the vote decides for the warp)
+    if (__any_sync(0xffffffffu, m0 > m[0] + LAZY || m1 > m[1] + LAZY || (FP8 && top > vref))) {
+      m0 = fmaxf(m[0], quad_max(m0));
+      m1 = fmaxf(m[1], quad_max(m1));
+      float ref = vref;
+      if (FP8) {
+        top = warp_max(top);
+        if (top > vref) ref = pow2(min(max(static_cast<int>(__float_as_uint(top) >> 23) - 126, -126), 126));
+      }
+      // ex2(-inf) = 0; a row that has seen no key yet keeps -inf
+      const float c0 = m0 == -INFINITY ? 0.f : ptx::ex2_approx(m[0] - m0);
+      const float c1 = m1 == -INFINITY ? 0.f : ptx::ex2_approx(m[1] - m1);
       const float vc = FP8 && ref != vref ? vref / ref : 1.f;
-      l[0] *= c0;
-      l[1] *= c1;
+      l[0] = make_float2(l[0].x * c0, l[0].y * c0);
+      l[1] = make_float2(l[1].x * c1, l[1].y * c1);
 #pragma unroll
       for (int k = 0; k < D / 8; ++k) {
         o[k][0] *= c0 * vc;
@@ -310,48 +331,40 @@ struct MhaRows {
       m[1] = m1;
       vref = ref;
     }
+    const float r0 = m[0] == -INFINITY ? 0.f : -m[0], r1 = m[1] == -INFINITY ? 0.f : -m[1];
     // 1 / vref: a power of two's reciprocal has the mirrored exponent
     const float inv = FP8 && vref > 0.f ? __uint_as_float(0x7F000000u - __float_as_uint(vref)) : 0.f;
-    uint32_t pa[KS][4];
 #pragma unroll
     for (int x = 0; x < 2 * KS; ++x) {
-      const float p00 = ptx::ex2_approx(s[x][0] - r0), p01 = ptx::ex2_approx(s[x][1] - r0);
-      const float p10 = ptx::ex2_approx(s[x][2] - r1), p11 = ptx::ex2_approx(s[x][3] - r1);
-      l[0] += p00 + p01;
-      l[1] += p10 + p11;
       uint32_t* a = &pa[x >> 1][(x & 1) * 2];
-      if (FP8) {
-        const float w0 = sv[x][0] * inv, w1 = sv[x][1] * inv;
-        a[0] = ptx::pack_f16x2(p00 * w0, p01 * w1);
-        a[1] = ptx::pack_f16x2(p10 * w0, p11 * w1);
-      } else {
-        a[0] = ptx::pack_bf16x2(p00, p01);
-        a[1] = ptx::pack_bf16x2(p10, p11);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float2 e = __fadd2_rn(s[x][u], u ? make_float2(r1, r1) : make_float2(r0, r0));
+        float2 w = make_float2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
+        l[u] = __fadd2_rn(l[u], w);
+        if (FP8) {
+          w = __fmul2_rn(w, __fmul2_rn(sv[x], make_float2(inv, inv)));
+          a[u] = ptx::pack_f16x2(w.x, w.y);
+        } else {
+          a[u] = ptx::pack_bf16x2(w.x, w.y);
+        }
       }
     }
-    // Rows of the cache past the request's end hold anything: their values are zeroed, since a weight of
-    // 0 does not silence an infinity.  keep: the two keys of a register that exist.
-    uint32_t keep[2 * KS];
-#pragma unroll
-    for (int x = 0; x < 2 * KS; ++x) keep[x] = 0xFFFFFFFFu;
-    if (key0 + 16 * KS > n) {
-#pragma unroll
-      for (int x = 0; x < 2 * KS; ++x) {
-        const uint32_t k0 = key0 + 8 * x + 2 * t;
-        keep[x] = (k0 < n ? 0xFFFFu : 0u) | (k0 + 1 < n ? 0xFFFF0000u : 0u);
-      }
-    }
-    const uint32_t r = row + (lane & 7) + ((lane >> 3) & 1) * 8;
-    const uint32_t half = (lane >> 4) * 16;
+  }
+
+  // O += weights * V; vcol, pitch as for scores.
+  template <int KS>
+  __device__ __forceinline__ void values(uint32_t vcol, uint32_t pitch, const uint32_t (&pa)[KS][4]) {
+    const uint32_t a0 = vcol + voff, a1 = a0 + pitch;
     if (!FP8) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
 #pragma unroll
         for (int y = 0; y < KS; ++y) {
           uint32_t vb[4];
-          ldsm4_t(at(vrun, rows, col + k * 32 / CW, r + 16 * y, (k * 32) % CW + half), vb);
-          mma_16816_bf16(o[2 * k], pa[y], vb[0] & keep[2 * y], vb[1] & keep[2 * y + 1]);
-          mma_16816_bf16(o[2 * k + 1], pa[y], vb[2] & keep[2 * y], vb[3] & keep[2 * y + 1]);
+          ldsm4_t(((k * 32 < CW ? a0 : a1) ^ ((k * 32) % CW)) + y * 16 * CW, vb);
+          mma_16816_bf16(o[2 * k], pa[y], vb[0], vb[1]);
+          mma_16816_bf16(o[2 * k + 1], pa[y], vb[2], vb[3]);
         }
     } else {
 #pragma unroll
@@ -359,10 +372,10 @@ struct MhaRows {
 #pragma unroll
         for (int y = 0; y < KS; ++y) {
           uint32_t vb[4];
-          ldsm4_t(at(vrun, rows, col, r + 16 * y, k * 32 + half), vb);
+          ldsm4_t((a0 ^ (k * 32)) + y * 16 * CW, vb);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint32_t a = vb[2 * x] & keep[2 * y], b = vb[2 * x + 1] & keep[2 * y + 1];
+            const uint32_t a = vb[2 * x], b = vb[2 * x + 1];
             mma_16816_f16(o[4 * k + 2 * x], pa[y], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(a, 0, 0x4420))),
                           ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(b, 0, 0x4420))));
             mma_16816_f16(o[4 * k + 2 * x + 1], pa[y], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(a, 0, 0x4431))),
@@ -370,6 +383,17 @@ struct MhaRows {
           }
         }
     }
+  }
+
+  // The last step of a request: rows of V past its end hold anything, and a weight of 0 does not silence an
+  // infinity.  Zeroes this head's part of rows `from` .. 16 KS - 1 (each warp for itself, before it reads).
+  template <int KS>
+  __device__ __forceinline__ void clear_tail(uint32_t vcol, uint32_t pitch, uint32_t from, int lane) const {
+    constexpr uint32_t UNITS = CW / 16, COLS = D * (FP8 ? 1 : 2) / CW;
+    for (uint32_t x = from * UNITS + lane; x < 16 * KS * UNITS; x += 32)
+#pragma unroll
+      for (uint32_t c = 0; c < COLS; ++c) ptx::st_shared_v4(vcol + c * pitch + x * 16, 0, 0, 0, 0);
+    __syncwarp();
   }
 
   // Adds another warp's state over other keys of the same rows (l already summed over the quad).
@@ -382,9 +406,9 @@ struct MhaRows {
     if ((lane & 3) == 0) {
       float* ml = buf + 16 * D + (lane >> 2) * 2;
       ml[0] = m[0];
-      ml[1] = l[0];
+      ml[1] = l[0].x;
       ml[16] = m[1];
-      ml[17] = l[1];
+      ml[17] = l[1].x;
     }
   }
   __device__ __forceinline__ void add(const float* buf, int lane) {
@@ -395,7 +419,7 @@ struct MhaRows {
       const float om = ml[16 * u], ol = ml[16 * u + 1], mm = fmaxf(m[u], om), ref = mm == -INFINITY ? 0.f : mm;
       mine[u] = ptx::ex2_approx(m[u] - ref);
       theirs[u] = ptx::ex2_approx(om - ref);
-      l[u] = l[u] * mine[u] + ol * theirs[u];
+      l[u].x = l[u].x * mine[u] + ol * theirs[u];
       m[u] = mm;
     }
 #pragma unroll
@@ -405,8 +429,8 @@ struct MhaRows {
         o[k][x] = o[k][x] * mine[x >> 1] + buf[lane + (4 * k + x) * 32] * theirs[x >> 1];
   }
   __device__ __forceinline__ void finish_sums() {
-    l[0] = quad_sum(l[0]);
-    l[1] = quad_sum(l[1]);
+    l[0].x = quad_sum(l[0].x + l[0].y);
+    l[1].x = quad_sum(l[1].x + l[1].y);
     if (FP8) {
 #pragma unroll
       for (int k = 0; k < D / 8; ++k)
@@ -427,19 +451,24 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t merge = p.stages * p.stage_bytes;
   const uint32_t sbar = merge + (p.kw > 1 ? mha_merge_bytes<D>() : 0);
-  const uint32_t sbad = sbar + 8 * 2 * MHA_MAX_STAGES;             // per stage: runs without a page
+  const uint32_t sbad = sbar + 8 * 4 * MHA_MAX_STAGES;             // per stage: runs without a page
   volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem + sbad + 4 * MHA_MAX_STAGES);
   int* start = reinterpret_cast<int*>(smem + sbad + 4 * MHA_MAX_STAGES + 16);   // request, item, tile
   long long* tot = reinterpret_cast<long long*>(smem + sbad + 4 * MHA_MAX_STAGES + 64);
-  auto full = [&](uint32_t s) { return base + sbar + 8 * s; };
-  auto empty = [&](uint32_t s) { return base + sbar + 8 * (MHA_MAX_STAGES + s); };
+  // K and V of a tile are handed over separately: K is free once its scores are formed, while its V waits
+  auto full_k = [&](uint32_t s) { return base + sbar + 8 * s; };
+  auto full_v = [&](uint32_t s) { return base + sbar + 8 * (MHA_MAX_STAGES + s); };
+  auto empty_k = [&](uint32_t s) { return base + sbar + 8 * (2 * MHA_MAX_STAGES + s); };
+  auto empty_v = [&](uint32_t s) { return base + sbar + 8 * (3 * MHA_MAX_STAGES + s); };
   const int active = p.hg * p.mt * p.kw;
   const int items = p.head_groups * p.row_groups;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      ptx::mbar_init(full(s), 1);
-      ptx::mbar_init(empty(s), active);
+      ptx::mbar_init(full_k(s), 1);
+      ptx::mbar_init(full_v(s), 1);
+      ptx::mbar_init(empty_k(s), active);
+      ptx::mbar_init(empty_v(s), active);
     }
     *abort = 0u;
     ptx::fence_mbar_init();
@@ -461,7 +490,7 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane == 0) tot[warp] = mine;
     __syncthreads();
-    for (int w = 0; w <= MHA_WARPS; ++w) all += tot[w];
+    for (int w = 0; w < MHA_THREADS / 32; ++w) all += tot[w];
     nc = min(static_cast<long long>(gridDim.x), all);    // no empty range among the first nc
     r0 = blockIdx.x < nc ? all * blockIdx.x / nc : all;
     r1 = blockIdx.x < nc ? all * (blockIdx.x + 1ll) / nc : all;
@@ -486,7 +515,7 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
         start[1] = static_cast<int>(in / nt);
         start[2] = static_cast<int>(in % nt);
       }
-      for (int w = 0; w <= MHA_WARPS; ++w) before += tot[w];
+      for (int w = 0; w < MHA_THREADS / 32; ++w) before += tot[w];
       __syncthreads();
     }
   }
@@ -496,14 +525,17 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
     return __all_sync(0xffffffffu, wait_bar(b, parity, abort, p.status, 0, lim)) != 0;
   };
 
-  if (warp == MHA_WARPS) {
-    // ------------------------------------------------------------------ producer
+  // 384 threads of 168 registers: the producer's warpgroup hands 112 a thread on to the
+  // consumers (8 warps x 224 + 4 x 56 = 12 x 168).
+  if (warp >= MHA_WARPS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // ------------------------------------------------------------------ producer (the group's first warp)
     uint32_t n = 0;                                      // tiles issued
     const int runs = p.tile / p.box_rows;
     const uint32_t sc_bytes = FP8 ? p.box_rows * p.HKV * 4u : 0u;
     const uint32_t box_bytes = p.hg * CPH * p.box_rows * Rows::CW;
     MhaPiece u;
-    bool live = true;
+    bool live = warp == MHA_WARPS;
     while (live && walk.next(p, u)) {
       const uint32_t stored = mha_length(p, u.b) + p.T;
       if (lane == 0 && u.ta == 0 && u.item == 0 && p.cache_lengths[u.b] > p.max_cache_length)
@@ -527,35 +559,43 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
         }
         const uint32_t bad = __ballot_sync(0xffffffffu, in && !have);
         const uint32_t got = __popc(__ballot_sync(0xffffffffu, have));
-        if (!wait(empty(s), (use & 1) ^ 1)) { live = false; break; }
+        const uint32_t dst = base + s * p.stage_bytes + lane * box_bytes, bytes = got * (box_bytes + sc_bytes);
+        const uint32_t sd = base + s * p.stage_bytes + 2 * p.plane_bytes + lane * sc_bytes;
+        const int plane_rows = p.NL * p.P;
+        // the weights need V's scales before V itself: they come, and go, with K
+        if (!wait(empty_k(s), (use & 1) ^ 1)) { live = false; break; }
         if (lane == 0) {
           ptx::st_shared_u32(base + sbad + 4 * s, bad);
-          ptx::mbar_arrive_expect_tx(full(s), got * 2 * (box_bytes + sc_bytes));
+          ptx::mbar_arrive_expect_tx(full_k(s), bytes + got * sc_bytes);
         }
         __syncwarp();
         if (have) {
-          const uint32_t dst = base + s * p.stage_bytes + lane * box_bytes;
-          const int plane_rows = p.NL * p.P;
-          ptx::tma_load_3d(dst, &p.tmap, 0, row, head0 * CPH, full(s));
-          ptx::tma_load_3d(dst + p.plane_bytes, &p.tmap, 0, row + plane_rows, head0 * CPH, full(s));
+          ptx::tma_load_3d(dst, &p.tmap, 0, row, head0 * CPH, full_k(s));
           if (FP8) {
-            const uint32_t sd = base + s * p.stage_bytes + 2 * p.plane_bytes + lane * sc_bytes;
-            ptx::bulk_load(sd, p.scales + srow * p.HKV, sc_bytes, full(s));
-            ptx::bulk_load(sd + p.tile * p.HKV * 4, p.scales + (srow + plane_rows) * p.HKV, sc_bytes, full(s));
+            ptx::bulk_load(sd, p.scales + srow * p.HKV, sc_bytes, full_k(s));
+            ptx::bulk_load(sd + p.tile * p.HKV * 4, p.scales + (srow + plane_rows) * p.HKV, sc_bytes, full_k(s));
           }
         }
+        if (!wait(empty_v(s), (use & 1) ^ 1)) { ++n; live = false; break; }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(full_v(s), got * box_bytes);
+        __syncwarp();
+        if (have) ptx::tma_load_3d(dst + p.plane_bytes, &p.tmap, 0, row + plane_rows, head0 * CPH, full_v(s));
       }
     }
     for (uint32_t s = 0; s < static_cast<uint32_t>(p.stages) && s < n; ++s)   // no copy may land after the CTA is gone
-      drain_bar(full(s), ((n - 1 - s) / p.stages) & 1, lim);
-  } else if (warp < active) {
+    {
+      drain_bar(full_k(s), ((n - 1 - s) / p.stages) & 1, 10000000ull);
+      drain_bar(full_v(s), ((n - 1 - s) / p.stages) & 1, 10000000ull);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // ------------------------------------------------------------------ consumers
     const int kp = warp / (p.hg * p.mt), pair = warp - kp * p.hg * p.mt;
     const int hl = pair / p.mt, rt = pair - hl * p.mt;   // kv head and row tile within the CTA
     Rows w;
     MhaPiece u;
-    uint32_t n = 0;
-    bool live = true;
+    uint32_t stk = 0, stv = 0, kpar = 0, vpar = 0;       // next K and V stage, and their phases
+    bool live = warp < active;
     int4 mine = make_int4(-1, 0, 0, 0);                  // the item this CTA holds the head of, if it is cut
     while (live && walk.next(p, u)) {
       const int hgi = u.item / p.row_groups, rgi = u.item - hgi * p.row_groups;
@@ -563,24 +603,80 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
       const bool work = kvh < p.HKV && row0 < p.R;
       const uint32_t stored = mha_length(p, u.b) + p.T;
       w.load_q(p, u.b, work ? kvh : 0, work ? row0 : p.R, lane);
-      for (int j = u.ta; j < u.tb; ++j, ++n) {
-        const uint32_t s = n % p.stages;
-        if (!wait(full(s), (n / p.stages) & 1)) { live = false; break; }
-        const uint32_t bad = ptx::ld_shared_u32(base + sbad + 4 * s);
-        const uint32_t kst = base + s * p.stage_bytes, vst = kst + p.plane_bytes;
-        const uint32_t sst = vst + p.plane_bytes;
-        const uint32_t box_bytes = p.hg * CPH * p.box_rows * Rows::CW;
-        for (int g = kp * 16 * KS; work && g < p.tile; g += p.kw * 16 * KS) {
-          const uint32_t key0 = static_cast<uint32_t>(j) * p.tile + g;
-          if (key0 >= stored) break;
-          const int run = g / p.box_rows, row = g - run * p.box_rows;
-          if ((bad >> run) & 1u) continue;               // no such page: its keys are left out
-          const uint32_t ks = sst + (g * p.HKV + kvh) * 4;
-          w.template step<KS>(p, kst + run * box_bytes, vst + run * box_bytes, p.box_rows, row, hl * CPH, ks,
-                 ks + p.tile * p.HKV * 4, key0, stored, lane);
+      // Steps of this warp: keys (kp + x kw) 16 KS of each tile.  The scores of the next step are formed
+      // beside the value product of this one: two independent streams of loads, conversions and MMAs.
+      const uint32_t pitch = p.box_rows * Rows::CW, box_bytes = p.hg * CPH * pitch, sstep = p.HKV * 4;
+      const uint32_t my_k = base + hl * CPH * pitch, my_s = base + 2 * p.plane_bytes + kvh * 4, vscales = p.tile * sstep;
+      struct Step {
+        uint32_t k, sc, key0;                            // addresses of its K and scales; first key
+        bool ok;                                         // has keys, and a page
+      };
+      auto locate = [&](uint32_t stage, int j, uint32_t g, uint32_t bad) {
+        Step t;
+        const uint32_t run = g >> p.box_shift, at = stage * p.stage_bytes;
+        t.key0 = static_cast<uint32_t>(j) * p.tile + g;
+        t.k = my_k + at + run * box_bytes + (g - (run << p.box_shift)) * Rows::CW;
+        t.sc = my_s + at + g * sstep;
+        t.ok = work && t.key0 < stored && !((bad >> run) & 1u);
+        return t;
+      };
+      auto enter = [&](uint32_t stage, uint32_t& bad) {  // K of the next tile (and V's scales) are in
+        if (!wait(full_k(stage), kpar)) return false;
+        bad = ptx::ld_shared_u32(base + sbad + 4 * stage);
+        return true;
+      };
+      const uint32_t g0 = kp * 16 * KS, gstep = p.kw * 16 * KS;
+      uint32_t bad = 0;
+      float2 s[2 * KS][2];
+      Step cur{};
+      if (u.ta < u.tb) {
+        if (!enter(stk, bad)) live = false;
+        cur = locate(stk, u.ta, g0, bad);
+        if (live && cur.ok) w.template scores<KS>(cur.k, pitch, s);
+      }
+      for (int j = u.ta; j < u.tb && live; ++j) {
+        bool have_v = false;
+        for (uint32_t g = g0; g < static_cast<uint32_t>(p.tile) && live; g += gstep) {
+          const bool end = g + gstep >= static_cast<uint32_t>(p.tile);   // this warp's last step of the tile
+          const bool more = !end || j + 1 < u.tb;
+          uint32_t pa[KS][4];
+          if (cur.ok) w.template weights<KS>(p, s, cur.sc, cur.sc + vscales, sstep, cur.key0, stored, lane, pa);
+          if (end) {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(empty_k(stk));   // the tile's K and scales are read
+            if (++stk == static_cast<uint32_t>(p.stages)) {
+              stk = 0;
+              kpar ^= 1;
+            }
+            if (more && !enter(stk, bad)) { live = false; break; }
+          }
+          if (!have_v) {
+            if (!wait(full_v(stv), vpar)) { live = false; break; }
+            have_v = true;
+          }
+          Step nxt = cur;
+          if (more) nxt = locate(stk, end ? j + 1 : j, end ? g0 : g + gstep, bad);
+          if (cur.ok) {
+            const uint32_t v = cur.k + p.plane_bytes;
+            if (cur.key0 + 16 * KS > stored) {
+              w.template clear_tail<KS>(v, pitch, stored - cur.key0, lane);
+              ptx::fence_proxy_async_smem();             // before the stage's next copy
+            }
+            // (the last step of a piece forms its own scores again: nothing reads them)
+            w.template scores<KS>(nxt.k, pitch, s);
+            w.template values<KS>(v, pitch, pa);
+          } else if (nxt.ok) {
+            w.template scores<KS>(nxt.k, pitch, s);
+          }
+          cur = nxt;
+          if (!more) cur.ok = false;
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(empty(s));
+        if (lane == 0) ptx::mbar_arrive(empty_v(stv));
+        if (++stv == static_cast<uint32_t>(p.stages)) {
+          stv = 0;
+          vpar ^= 1;
+        }
       }
       w.finish_sums();
       if (p.kw > 1) {
@@ -608,8 +704,8 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
         for (int v = 0; v < 2; ++v) {
           const int r = row0 + (lane >> 2) + 8 * v, t = lane & 3;
           if (r >= p.R) continue;
-          const float inv = w.l[v] > 0.f || w.l[v] != w.l[v] ? 1.f / w.l[v] : 0.f;
-          const float lse2 = w.l[v] > 0.f || w.l[v] != w.l[v] ? w.m[v] + log2f(w.l[v]) : -INFINITY;
+          const float inv = w.l[v].x > 0.f || w.l[v].x != w.l[v].x ? 1.f / w.l[v].x : 0.f;
+          const float lse2 = w.l[v].x > 0.f || w.l[v].x != w.l[v].x ? w.m[v] + log2f(w.l[v].x) : -INFINITY;
           if (whole) {
             const int i = static_cast<int>(p.divG.div(r));
             const size_t row = (static_cast<size_t>(u.b) * p.T + i) * p.H + kvh * p.divG.d + (r - i * p.divG.d);
@@ -645,7 +741,7 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
         }
       }
     }
-    if (!p.one_item && warp == 0 && lane == 0) p.desc[blockIdx.x] = live ? mine : make_int4(-1, 0, 0, 0);
+    if (!p.one_item && warp == 0 && lane == 0) p.desc[blockIdx.x] = !*abort ? mine : make_int4(-1, 0, 0, 0);
   }
   ptx::griddep_launch_dependents();
 }
