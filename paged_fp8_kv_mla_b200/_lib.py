@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -423,11 +424,13 @@ def _allocating_on(stream, device):
                              else torch.cuda.ExternalStream(_raw_stream(stream, device), torch.device("cuda", device)))
 
 
-def _scratch(n, device, stream):
+def _scratch(n, like, device, stream):
+    if not n:
+        return None
     if stream is None:
-        return torch.empty(n, dtype=_U8, device=torch.device("cuda", device)) if n else None
+        return torch.empty(n, dtype=_U8, device=like.device)
     with _allocating_on(stream, device):
-        return torch.empty(n, dtype=_U8, device=torch.device("cuda", device)) if n else None
+        return torch.empty(n, dtype=_U8, device=like.device)
 
 
 def _check_tables(cache_lengths, lookup_table, scales_lookup_table, batch):
@@ -492,7 +495,7 @@ def accumulate_weights(q, lse, blocks, scales, cache_lengths, lookup_table, scal
         else:
             out, ostep = scores, sstep
     if workspace is None:
-        workspace = _scratch(accumulate_workspace_bytes(B, T, H), dev, stream)
+        workspace = _scratch(accumulate_workspace_bytes(B, T, H), q, dev, stream)
     _run(dev, lib.mla_accumulate_weights_fp8, q.data_ptr(), lse.data_ptr(), blocks.data_ptr(), scales.data_ptr(),
          cache_lengths.data_ptr(), lookup_table.data_ptr(), _adr(scales_lookup_table), T, int(max_cache_length), int(layer_idx),
          float(softmax_scale), ctypes.byref(shp), _adr(scores), sstep, out.data_ptr(), ostep, _adr(workspace),
@@ -500,6 +503,7 @@ def accumulate_weights(q, lse, blocks, scales, cache_lengths, lookup_table, scal
     return out
 
 
+@functools.lru_cache(maxsize=1024)      # a function of the sizes alone
 def accumulate_workspace_bytes(batch: int, max_prompt_length: int, num_q_heads: int) -> int:
     """Bytes of workspace that accumulate_weights needs."""
     n, shp = ctypes.c_uint64(0), PagedShape(batch, num_q_heads)
@@ -644,10 +648,8 @@ def mha_decode(q, blocks, scales, cache_lengths, lookup_table, scales_lookup_tab
             if lse is None and want_lse:
                 lse = torch.empty((B, T, H), dtype=_F32, device=q.device)
     if workspace is None:
-        n = ctypes.c_uint64(0)
-        _run(dev, lib.mla_mha_decode_workspace_bytes, T, int(max_cache_length), blocks.element_size(), ctypes.byref(shp),
-             ctypes.byref(n))
-        workspace = _scratch(n.value, dev, stream)
+        workspace = _scratch(_mha_workspace(dev, T, int(max_cache_length), blocks.element_size(), B, H, D, shp.num_kv_heads,
+                                            shp.page_size, shp.max_pages), q, dev, stream)
     _run(dev, lib.mla_mha_decode_paged, q.data_ptr(), blocks.data_ptr(), _adr(scales), cache_lengths.data_ptr(),
          lookup_table.data_ptr(), _adr(scales_lookup_table), T, int(max_cache_length), int(layer_idx), float(softmax_scale),
          blocks.element_size(), ctypes.byref(shp), out.data_ptr(), _adr(lse), _adr(workspace),
@@ -655,14 +657,19 @@ def mha_decode(q, blocks, scales, cache_lengths, lookup_table, scales_lookup_tab
     return out, lse
 
 
+@functools.lru_cache(maxsize=4096)      # a function of the device and the sizes alone
+def _mha_workspace(device, T, max_cache_length, element_bytes, B, H, D, HKV, P, max_pages):
+    shp = PagedShape(B, H, D, D, 1, 2, 1, P, HKV, 1, 1, max_pages)
+    n = ctypes.c_uint64(0)
+    _run(device, load().mla_mha_decode_workspace_bytes, T, max_cache_length, element_bytes, ctypes.byref(shp), ctypes.byref(n))
+    return n.value
+
+
 def mha_decode_workspace_bytes(q, blocks, lookup_table, max_cache_length: int) -> int:
     """Bytes of workspace that mha_decode needs for these tensors (0 for short caches)."""
-    NB, KVD, NL, P, NKV, D = blocks.shape
-    shp = PagedShape(q.shape[0], q.shape[2], D, D, NB, KVD, NL, P, NKV, NB, 1, lookup_table.shape[1])
-    n = ctypes.c_uint64(0)
-    _run(q.get_device(), load().mla_mha_decode_workspace_bytes, q.shape[1], int(max_cache_length), blocks.element_size(),
-         ctypes.byref(shp), ctypes.byref(n))
-    return n.value
+    B, T, H, D = q.shape
+    return _mha_workspace(q.get_device(), T, int(max_cache_length), blocks.element_size(), B, H, D, blocks.shape[4],
+                          blocks.shape[3], lookup_table.shape[1])
 
 
 def set_num_clusters(n: int):

@@ -12,9 +12,10 @@ namespace {
 
 int gcd_int(int a, int b) { return b == 0 ? a : gcd_int(b, a % b); }
 
-// Current device, its SM count, and (once per device) the shared-memory limits of the kernels here.
-mla_status_t cache_device(int* sms) {
+// The current device's SM count and status word, and (once per device) the shared-memory limits of the kernels here.
+mla_status_t cache_device(int* sms, unsigned int** status) {
   static int g_sms[kMaxDevices];
+  static unsigned int* g_status[kMaxDevices];
   int dev = 0;
   MLA_CUDA(cudaGetDevice(&dev));
   if (dev >= kMaxDevices) return fail(MLA_ERR_UNSUPPORTED, "device index too large");
@@ -26,7 +27,8 @@ mla_status_t cache_device(int* sms) {
       return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     };
     MLA_CUDA(smem(mla::mla_accumulate_kernel, mla::ACC_SMEM_ALLOC));
-    MLA_CUDA(smem(mla::mla_select_kernel, mla::SEL_KEYS_OFF + mla::SEL_CACHE * 4));
+    MLA_CUDA(smem(mla::mla_select_kernel<512>, mla::SEL_KEYS_OFF + mla::SEL_CACHE * 4));
+    MLA_CUDA(smem(mla::mla_select_kernel<1024>, mla::SEL_KEYS_OFF + mla::SEL_CACHE * 4));
     MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, false, 1>, mla::MHA_SMEM_LIMIT));
     MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, false, 2>, mla::MHA_SMEM_LIMIT));
     MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, true, 1>, mla::MHA_SMEM_LIMIT));
@@ -35,8 +37,11 @@ mla_status_t cache_device(int* sms) {
     MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, false, 2>, mla::MHA_SMEM_LIMIT));
     MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, true, 1>, mla::MHA_SMEM_LIMIT));
     MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, true, 2>, mla::MHA_SMEM_LIMIT));
+    g_status[dev] = status_ptr();
+    if (!g_status[dev]) return fail(MLA_ERR_CUDA, "status word address unavailable");
     g_sms[dev] = n;
   }
+  *status = g_status[dev];
   *sms = g_sms[dev];
   return MLA_OK;
 }
@@ -259,7 +264,8 @@ mla_status_t mla_accumulate_weights_fp8(const void* q, const float* lse, const v
   if (d.B == 0) return MLA_OK;
   if (static_cast<int64_t>(d.T) * d.G > 0x3FFFFFFF) return fail(MLA_ERR_UNSUPPORTED, "too many query tokens");
   int sms = 0;
-  st = cache_device(&sms);
+  unsigned int* status = nullptr;
+  st = cache_device(&sms, &status);
   if (st != MLA_OK) return st;
   mla::AccumulateParams p{};
   p.box_rows = gcd_int(d.P, mla::ACC_BN);
@@ -286,8 +292,7 @@ mla_status_t mla_accumulate_weights_fp8(const void* q, const float* lse, const v
   p.out = out;
   p.scores_stride = scores_stride;
   p.out_stride = out_stride;
-  p.status = status_ptr();
-  if (!p.status) return fail(MLA_ERR_CUDA, "status word address unavailable");
+  p.status = status;
   p.B = d.B;
   p.T = d.T;
   p.H = d.H;
@@ -358,30 +363,32 @@ mla_status_t mla_select_keys(const float* scores, int64_t scores_stride, const u
   if (kept_stride < most) return fail(MLA_ERR_INVALID_ARG, "the rows of kept must hold %lld values", static_cast<long long>(most));
   if (batch == 0) return MLA_OK;
   int sms = 0;
-  mla_status_t st = cache_device(&sms);
+  unsigned int* status = nullptr;
+  mla_status_t st = cache_device(&sms, &status);
   if (st != MLA_OK) return st;
   mla::SelectParams p{};
   p.scores = scores;
   p.lengths = lengths;
   p.kept = kept;
   p.kept_lengths = kept_lengths;
-  p.status = status_ptr();
-  if (!p.status) return fail(MLA_ERR_CUDA, "status word address unavailable");
+  p.status = status;
   p.scores_stride = scores_stride;
   p.kept_stride = kept_stride;
   p.max_length = max_length;
   p.budget = budget;
   p.recent = num_recent;
   p.sink = num_sink;
-  // CTAs per request: about 2048 keys each, up to the portable cluster size.
+  // CTAs per request: about 2048 keys each, up to the portable cluster size, while all of them fit on the
+  // device at once (128 requests of 8k: 18 us with 2, 30 with 4 in two waves); of 512 threads, and of 1024
+  // where a CTA has more than 8192 keys (4 of 128k: 25 us, 30 with 512; 32 of 4k: 15.4, 13.4 with 512).
   int ncta = 1;
-  while (ncta < 8 && static_cast<uint32_t>(ncta) * 2048 < max_length) ncta *= 2;
+  while (ncta < 8 && static_cast<uint32_t>(ncta) * 2048 < max_length && static_cast<int64_t>(batch) * ncta * 2 <= 2 * sms) ncta *= 2;
   if (static_cast<int64_t>(batch) * ncta > 0x7FFFFFFF) return fail(MLA_ERR_UNSUPPORTED, "batch too large");
   const uint32_t per = (max_length + ncta - 1) / ncta;
   const uint32_t cached = per < static_cast<uint32_t>(mla::SEL_CACHE) ? per : mla::SEL_CACHE;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(batch) * ncta);
-  cfg.blockDim = dim3(mla::SEL_THREADS);
+  cfg.blockDim = dim3(per > 8192 ? 1024 : 512);
   cfg.dynamicSmemBytes = mla::SEL_KEYS_OFF + cached * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -391,7 +398,10 @@ mla_status_t mla_select_keys(const float* scores, int64_t scores_stride, const u
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  MLA_CUDA(cudaLaunchKernelEx(&cfg, mla::mla_select_kernel, p));
+  if (per > 8192)
+    MLA_CUDA(cudaLaunchKernelEx(&cfg, mla::mla_select_kernel<1024>, p));
+  else
+    MLA_CUDA(cudaLaunchKernelEx(&cfg, mla::mla_select_kernel<512>, p));
   return MLA_OK;
 }
 
@@ -421,7 +431,8 @@ mla_status_t mla_compact_paged(const int32_t* kept, int64_t kept_stride, int32_t
   if (s->batch == 0) return MLA_OK;
   if (s->batch > 65535) return fail(MLA_ERR_UNSUPPORTED, "batch must be at most 65535");
   int sms = 0;
-  st = cache_device(&sms);
+  unsigned int* status = nullptr;
+  st = cache_device(&sms, &status);
   if (st != MLA_OK) return st;
   mla::CompactParams p{};
   p.kept = kept;
@@ -431,8 +442,7 @@ mla_status_t mla_compact_paged(const int32_t* kept, int64_t kept_stride, int32_t
   p.blocks = static_cast<uint8_t*>(blocks);
   p.scales = scales;
   p.scores = scores;
-  p.status = status_ptr();
-  if (!p.status) return fail(MLA_ERR_CUDA, "status word address unavailable");
+  p.status = status;
   p.kept_stride = kept_stride;
   p.scores_stride = scores_stride;
   p.max_kept = max_kept;
@@ -448,16 +458,21 @@ mla_status_t mla_compact_paged(const int32_t* kept, int64_t kept_stride, int32_t
   p.row_words = static_cast<int>(row_words);
   p.divP = make_fastdiv(static_cast<uint32_t>(s->page_size));
   p.divW = make_fastdiv(static_cast<uint32_t>(row_words));
-  // 64-byte slices where they already give every SM a CTA, else 32-byte slices (a DRAM sector)
-  const bool narrow = row_bytes % 64 != 0 || static_cast<int64_t>(s->batch) * s->kv_dim * (row_bytes / 64) < sms;
+  // Slices of 64 bytes where they give every SM a CTA, else of 32 bytes; those in CTAs of 512 threads where
+  // there are more of them than SMs, else of 1024.  (12 requests of 30k: 63 us with 512, 71 with 1024;
+  // 4 of 128k: 192 and 146.)
+  const int64_t planes = static_cast<int64_t>(s->batch) * s->kv_dim;
+  const bool narrow = row_bytes % 64 != 0 || planes * (row_bytes / 64) < sms;
   p.slices = static_cast<int>(row_bytes / (narrow ? 32 : 64));
   const int64_t gx = static_cast<int64_t>(s->kv_dim) * (p.slices + 1) + 1;
   if (gx > 0x7FFFFFFF) return fail(MLA_ERR_UNSUPPORTED, "grid too large");
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(s->batch));
-  if (narrow)
-    mla::mla_compact_kernel<32><<<grid, mla::CMP_THREADS, 0, stream>>>(p);
+  if (!narrow)
+    mla::mla_compact_kernel<64, 256, 4><<<grid, 256, 0, stream>>>(p);
+  else if (planes * p.slices > sms)
+    mla::mla_compact_kernel<32, 512, 4><<<grid, 512, 0, stream>>>(p);
   else
-    mla::mla_compact_kernel<64><<<grid, mla::CMP_THREADS, 0, stream>>>(p);
+    mla::mla_compact_kernel<32, 1024, 4><<<grid, 1024, 0, stream>>>(p);
   MLA_CUDA(cudaGetLastError());
   return MLA_OK;
 }
@@ -474,6 +489,10 @@ mla_status_t mla_mha_kv_store(const void* k, const void* v, const uint32_t* cach
   if (!k || !v) return fail(MLA_ERR_INVALID_ARG, "k and v must be non-NULL");
   if (!aligned16(k) || !aligned16(v)) return fail(MLA_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
   if (tokens >= (1ull << 31)) return fail(MLA_ERR_UNSUPPORTED, "too many new tokens (%llu)", static_cast<unsigned long long>(tokens));
+  int sms = 0;
+  unsigned int* status = nullptr;
+  st = cache_device(&sms, &status);
+  if (st != MLA_OK) return st;
   p.tokens = static_cast<unsigned int>(tokens);
   p.chunks = s->num_kv_heads * s->head_dim / 8;
   p.k = static_cast<const uint16_t*>(k);
@@ -483,8 +502,7 @@ mla_status_t mla_mha_kv_store(const void* k, const void* v, const uint32_t* cach
   p.slut = scales_lookup_table;
   p.blocks = static_cast<uint8_t*>(blocks);
   p.scales = scales;
-  p.status = status_ptr();
-  if (!p.status) return fail(MLA_ERR_CUDA, "status word address unavailable");
+  p.status = status;
   p.B = s->batch;
   p.T = static_cast<int>(num_new_tokens);
   p.HKV = s->num_kv_heads;
@@ -510,7 +528,8 @@ mla_status_t mla_mha_decode_workspace_bytes(uint32_t max_prompt_length, uint32_t
   if (st != MLA_OK) return st;
   if (s->batch == 0) return MLA_OK;
   int sms = 0;
-  st = cache_device(&sms);
+  unsigned int* status = nullptr;
+  st = cache_device(&sms, &status);
   if (st != MLA_OK) return st;
   MhaPlan m{};
   st = mha_plan(s, max_prompt_length, max_cache_length, element_bytes, sms, &m);
@@ -533,7 +552,8 @@ mla_status_t mla_mha_decode_paged(const void* q, const void* blocks, const float
   MhaPlan m{};
   if (s->batch == 0) return mha_plan(s, max_prompt_length, max_cache_length, element_bytes, 1, &m);
   int sms = 0;
-  st = cache_device(&sms);
+  unsigned int* status = nullptr;
+  st = cache_device(&sms, &status);
   if (st != MLA_OK) return st;
   st = mha_plan(s, max_prompt_length, max_cache_length, element_bytes, sms, &m);
   if (st != MLA_OK) return st;
@@ -560,8 +580,7 @@ mla_status_t mla_mha_decode_paged(const void* q, const void* blocks, const float
     p.part_lse = reinterpret_cast<float*>(w + m.part_lse_off);
     p.desc = reinterpret_cast<int4*>(w + m.desc_off);
   }
-  p.status = status_ptr();
-  if (!p.status) return fail(MLA_ERR_CUDA, "status word address unavailable");
+  p.status = status;
   {
     std::lock_guard<std::mutex> lk(g_mu);
     p.wait_limit_ns = g_wait_limit_ns;

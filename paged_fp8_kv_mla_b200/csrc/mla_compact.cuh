@@ -14,8 +14,11 @@
 //
 // What bounds it: HBM, one read and one write of every moved row.  The slices of a request are
 // neighbouring CTAs, which walk the rows at the same pace, so the 128-byte lines they share are
-// fetched once.  A request has 9 slices of 576 bytes; with few requests the slices are 32 bytes wide
-// (a DRAM sector), twice as many CTAs.
+// fetched once.  A request has 9 slices of 576 bytes, four CTAs of 256 threads to an SM (128 requests of 8k
+// cut to 4k: 119 us, 0.79 of the copy rate; two of 512: 128).  With few requests the slices are 32 bytes wide
+// (a DRAM sector) and the CTAs larger, and what is in flight per SM bounds it (4 requests of 128k cut to
+// 64k: 146 us, 0.32; a cluster per slice, whose barrier waits for the writes, gave 141 and cost the full
+// batches 13 %).
 #pragma once
 #include <cstdint>
 #include "mla_kernels.cuh"
@@ -39,7 +42,6 @@ struct CompactParams {
   FastDiv divP, divW;              // by the page size and by row_words
 };
 
-constexpr int CMP_THREADS = 512;
 
 // Plain loads through L2, kept on their side of the chunk's barrier.
 __device__ __forceinline__ uint4 ld_row(const uint4* p) {
@@ -64,16 +66,16 @@ struct CompactColumn {
 };
 
 // Moves the column for rows 0 .. m - 1, `per_row` elements each, U elements per thread and chunk.
-template <typename V, int U, typename RowOf>
+template <typename V, int THREADS, int U, typename RowOf>
 __device__ __forceinline__ void compact_walk(const CompactParams& p, const int32_t* kept, uint32_t m, uint32_t per_row,
                                              RowOf row_of, const CompactColumn<V>& col) {
   const uint32_t total = m * per_row;
-  for (uint32_t e0 = 0; e0 < total; e0 += U * CMP_THREADS) {
+  for (uint32_t e0 = 0; e0 < total; e0 += U * THREADS) {
     // three rounds of independent loads: the kept indices, the page ids, the rows
     uint32_t to[U], x[U], from[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t e = e0 + u * CMP_THREADS + threadIdx.x;
+      const uint32_t e = e0 + u * THREADS + threadIdx.x;
       to[u] = row_of(min(e, total - 1));
       x[u] = min(e, total - 1) - to[u] * per_row;
       from[u] = e < total ? static_cast<uint32_t>(kept[to[u]]) : to[u];
@@ -118,11 +120,11 @@ __device__ __forceinline__ void compact_walk(const CompactParams& p, const int32
 // lane and chunk.  The three dependent rounds of a chunk overlap with the chunks before it: while chunk n
 // waits for its barrier and is written, chunk n + 1's rows are on their way and chunk n + 2's pages are
 // looked up.  (Its rows may be read before chunk n is written: they lie at or above chunk n + 1.)
-template <int SLICE, int U>
+template <int SLICE, int THREADS, int U>
 __device__ __forceinline__ void compact_rows(const CompactParams& p, const int32_t* kept, uint32_t m, const uint32_t* lut,
                                              int plane, int slice) {
   constexpr int LPR = SLICE / 16;                        // lanes per row
-  constexpr uint32_t ROWS = CMP_THREADS / LPR;           // rows of a chunk per step u
+  constexpr uint32_t ROWS = THREADS / LPR;           // rows of a chunk per step u
   constexpr uint32_t CHUNK = ROWS * U;
   constexpr uint32_t NONE = ~0u;
   uint8_t* base = p.blocks + slice * SLICE + (threadIdx.x & (LPR - 1)) * 16;
@@ -184,8 +186,8 @@ __device__ __forceinline__ void compact_rows(const CompactParams& p, const int32
 }
 
 // grid (kv planes * slices + kv planes (scales) + 1 (accumulated weights), requests)
-template <int SLICE>
-__global__ void __launch_bounds__(CMP_THREADS, 2) mla_compact_kernel(const __grid_constant__ CompactParams p) {
+template <int SLICE, int THREADS, int U>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) mla_compact_kernel(const __grid_constant__ CompactParams p) {
   const int b = blockIdx.y;
   const int32_t given = p.kept_lengths[b];
   const uint32_t m = min(max(given, 0), p.max_kept);
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(CMP_THREADS, 2) mla_compact_kernel(const __gri
   int i = blockIdx.x;
   if (i < p.KVD * p.slices) {
     const int plane = i / p.slices, slice = i - plane * p.slices;
-    compact_rows<SLICE, 4>(p, kept, m, lut, plane, slice);
+    compact_rows<SLICE, THREADS, U>(p, kept, m, lut, plane, slice);
     return;
   }
   i -= p.KVD * p.slices;
@@ -205,13 +207,13 @@ __global__ void __launch_bounds__(CMP_THREADS, 2) mla_compact_kernel(const __gri
     if (!p.scales) return;
     const CompactColumn<uint32_t> col{reinterpret_cast<uint32_t*>(p.scales), p.row_words, slut,
                                       static_cast<uint32_t>(p.NSB), static_cast<uint32_t>(i), ~0u};
-    compact_walk<uint32_t, 8>(p, kept, m, p.row_words, [&](uint32_t e) { return p.divW.div(e); }, col);
+    compact_walk<uint32_t, THREADS, 8>(p, kept, m, p.row_words, [&](uint32_t e) { return p.divW.div(e); }, col);
     return;
   }
   if (!p.scores) return;
   const CompactColumn<uint32_t> col{reinterpret_cast<uint32_t*>(p.scores + b * p.scores_stride), 1, nullptr, 0u, 0u,
                                     static_cast<uint32_t>(p.scores_cols)};
-  compact_walk<uint32_t, 8>(p, kept, m, 1, [](uint32_t e) { return e; }, col);
+  compact_walk<uint32_t, THREADS, 8>(p, kept, m, 1, [](uint32_t e) { return e; }, col);
 }
 
 }  // namespace mla

@@ -48,7 +48,7 @@ def test_select(lengths, budget, recent, sink, kind):
 
 
 def test_select_more_keys_than_a_cluster_holds():
-    """Past 8 x 40960 keys a CTA reads part of its keys again instead of holding them."""
+    """Past some 300 000 keys a CTA reads part of its keys again instead of holding them."""
     n, budget = 400_001, 100_000
     x = weights(1, n, 3, "ties")
     got, count = M.select_keys(x.cuda(), torch.tensor([n], dtype=torch.int32).cuda(), n, budget, 7, 3)
