@@ -12,6 +12,18 @@ namespace {
 
 int gcd_int(int a, int b) { return b == 0 ? a : gcd_int(b, a % b); }
 
+template <int D, bool FP8>
+cudaError_t mha_smem() {
+  auto set = [](auto* kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(mla::MHA_SMEM_LIMIT));
+  };
+  cudaError_t e = set(mla::mla_mha_decode_kernel<D, FP8, 1, 1>);
+  if (e == cudaSuccess) e = set(mla::mla_mha_decode_kernel<D, FP8, 2, 1>);
+  if (e == cudaSuccess) e = set(mla::mla_mha_decode_kernel<D, FP8, 1, 2>);
+  if (e == cudaSuccess) e = set(mla::mla_mha_decode_kernel<D, FP8, 2, 2>);
+  return e;
+}
+
 // The current device's SM count and status word, and (once per device) the shared-memory limits of the kernels here.
 mla_status_t cache_device(int* sms, unsigned int** status) {
   static int g_sms[kMaxDevices];
@@ -29,14 +41,10 @@ mla_status_t cache_device(int* sms, unsigned int** status) {
     MLA_CUDA(smem(mla::mla_accumulate_kernel, mla::ACC_SMEM_ALLOC));
     MLA_CUDA(smem(mla::mla_select_kernel<512>, mla::SEL_KEYS_OFF + mla::SEL_CACHE * 4));
     MLA_CUDA(smem(mla::mla_select_kernel<1024>, mla::SEL_KEYS_OFF + mla::SEL_CACHE * 4));
-    MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, false, 1>, mla::MHA_SMEM_LIMIT));
-    MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, false, 2>, mla::MHA_SMEM_LIMIT));
-    MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, true, 1>, mla::MHA_SMEM_LIMIT));
-    MLA_CUDA(smem(mla::mla_mha_decode_kernel<64, true, 2>, mla::MHA_SMEM_LIMIT));
-    MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, false, 1>, mla::MHA_SMEM_LIMIT));
-    MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, false, 2>, mla::MHA_SMEM_LIMIT));
-    MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, true, 1>, mla::MHA_SMEM_LIMIT));
-    MLA_CUDA(smem(mla::mla_mha_decode_kernel<128, true, 2>, mla::MHA_SMEM_LIMIT));
+    MLA_CUDA((mha_smem<64, false>()));
+    MLA_CUDA((mha_smem<64, true>()));
+    MLA_CUDA((mha_smem<128, false>()));
+    MLA_CUDA((mha_smem<128, true>()));
     g_status[dev] = status_ptr();
     if (!g_status[dev]) return fail(MLA_ERR_CUDA, "status word address unavailable");
     g_sms[dev] = n;
@@ -133,7 +141,7 @@ mla_status_t acc_plan(int64_t B, int64_t T, int64_t H, AccPlan* out) {
 
 // How a multi-head decode is laid out (the rules the kernel's header comment describes).
 struct MhaPlan {
-  int R, hg, mt, kw, ks, head_groups, row_groups, tile, box_rows, stages, NC, one_item;
+  int R, nr, hg, mt, kw, ks, head_groups, row_groups, tile, box_rows, stages, NC, one_item;
   uint32_t plane_bytes, stage_bytes, smem;
   uint64_t part_lse_off, desc_off, total;
 };
@@ -155,7 +163,8 @@ mla_status_t mha_plan(const mla_paged_shape_t* s, uint32_t T, uint32_t max_cache
   if (R > (1u << 24)) return fail(MLA_ERR_UNSUPPORTED, "too many query rows per kv head");
   m.R = static_cast<int>(R);
   // Warps: first the row tiles of a head (they share its keys), then heads, then the keys of a tile.
-  const int row_tiles = (m.R + 15) / 16;
+  m.nr = m.R <= 8 ? 1 : 2;
+  const int row_tiles = (m.R + 8 * m.nr - 1) / (8 * m.nr);
   m.mt = row_tiles < mla::MHA_WARPS ? row_tiles : mla::MHA_WARPS;
   m.row_groups = (row_tiles + m.mt - 1) / m.mt;
   const int most = mla::MHA_WARPS / m.mt;
@@ -198,14 +207,13 @@ mla_status_t mha_plan(const mla_paged_shape_t* s, uint32_t T, uint32_t max_cache
 
 template <int D, bool FP8>
 mla_status_t mha_launch(const mla::MhaParams& p, const MhaPlan& m, cudaStream_t stream) {
-  if (m.ks == 2)
-    mla::mla_mha_decode_kernel<D, FP8, 2><<<m.NC, mla::MHA_THREADS, m.smem, stream>>>(p);
-  else
-    mla::mla_mha_decode_kernel<D, FP8, 1><<<m.NC, mla::MHA_THREADS, m.smem, stream>>>(p);
+  auto* kernel = m.nr == 1 ? (m.ks == 2 ? mla::mla_mha_decode_kernel<D, FP8, 2, 1> : mla::mla_mha_decode_kernel<D, FP8, 1, 1>)
+                           : (m.ks == 2 ? mla::mla_mha_decode_kernel<D, FP8, 2, 2> : mla::mla_mha_decode_kernel<D, FP8, 1, 2>);
+  kernel<<<m.NC, mla::MHA_THREADS, m.smem, stream>>>(p);
   MLA_CUDA(cudaGetLastError());
   if (m.one_item) return MLA_OK;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(m.NC, static_cast<unsigned>((m.hg * m.mt * 16 + 7) / 8));
+  cfg.gridDim = dim3(m.NC, static_cast<unsigned>(m.hg * m.mt * m.nr));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -601,6 +609,7 @@ mla_status_t mla_mha_decode_paged(const void* q, const void* blocks, const float
   p.hg = m.hg;
   p.mt = m.mt;
   p.kw = m.kw;
+  p.row_tile = 8 * m.nr;
   p.head_groups = m.head_groups;
   p.row_groups = m.row_groups;
   p.tile = m.tile;

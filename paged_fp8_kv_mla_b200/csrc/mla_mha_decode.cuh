@@ -7,24 +7,23 @@
 // What bounds it.  A kv head's key and value are 4 D bytes (bf16) for 4 D flop per query row, so up to
 // some hundred rows per kv head the cache's bytes set the time: every K and V byte is to cross HBM once,
 // at full rate, and the arithmetic has to stay out of the way.  The rows that share a kv head
-// (R = T * G of them) are few, so the products run on the warp-level 16 x 8 x 16 MMA with 16 rows per
-// warp: a tcgen05 tile has 128 rows, most of them empty here, and its accumulator would have to come
-// back from tensor memory for every rescale.
+// (R = T * G of them) are few, so the products run on the warp-level 16 x 8 x 16 MMA with the query rows
+// as its 8 columns: a tcgen05 tile has 128 rows, most of them empty here, and its accumulator would have
+// to come back from tensor memory for every rescale.
 //
-// Who does what.  Eight consumer warps per CTA (one CTA per SM).  A warp owns 16 rows of one kv head
-// (its scores, weights and O stay in its registers; no exchange within a tile) and, where fewer than
-// eight (head, row tile) pairs exist, every kw-th group of 16 keys; those kw warps merge once, at the
-// end of a piece.  All warps read the same tile, so K and V are loaded once for all of up to 128 rows,
-// and a tile's rows are read as whole contiguous runs of the page over the CTA's heads.  A ninth warp
-// keeps a ring of tiles full by TMA: one box per page run and plane, [column of 128 (64) bytes][key],
-// in the matching shared-memory swizzle, so that ldmatrix reads rows without bank conflicts.
+// Who does what.  Eight consumer warps per CTA (one CTA per SM).  A warp owns 8 rows of one kv head (16
+// where the head has more than 8; its scores, weights and O stay in its registers, no exchange within a
+// tile) and, where fewer than eight (head, row tile) pairs exist, every kw-th group of keys; those kw warps
+// merge once, at the end of a piece.  All warps read the same tile, so K and V are loaded once for all of
+// up to 128 rows, and a tile's rows are read as whole contiguous runs of the page over the CTA's heads.  A
+// ninth warp keeps a ring of tiles full by TMA: one box per page run and plane, [column of 128 (64)
+// bytes][key], in the matching shared-memory swizzle, so that ldmatrix reads rows without bank conflicts.
 //
 // e4m3.  The values are converted to f16, exactly, as they leave shared memory (two per instruction),
-// and never to anything wider: q is brought to f16 with a power of two per row (exact down to 2^-30 of
-// the row's largest value), K's scale multiplies the score, and V's scale goes into the weight, relative
-// to a running power-of-two bound of V's scales so that f16 holds it with 11 bits.  A thread's four
-// consecutive bytes serve as the two k pairs of its MMA fragment, which only permutes the order of the
-// sum over dims (q is permuted the same way).
+// and never to anything wider: q is brought to f16 with a power of two (exact down to 2^-30 of the
+// largest value), K's scale multiplies the score, and V's scale goes into the weight, relative to a
+// running power-of-two bound of V's scales so that f16 holds it with 11 bits.  The instructions of this
+// are what keeps an e4m3 cache from the copy rate: the loads alone run at it.
 //
 // Work split.  The tiles of all (request, head group, row group) items laid end to end are cut into
 // equal contiguous ranges, one per CTA.  An item cut by a range's end leaves normalised fp32 partials
@@ -62,6 +61,7 @@ struct MhaParams {
   int B, T, H, HKV, R, P, KVD, NL, layer, NB, NSB, max_pages;
   unsigned int max_cache_length;
   int hg, mt, kw;                  // kv heads per CTA, row tiles per CTA, warps over the keys of a tile
+  int row_tile;                    // rows of a warp: 8 or 16
   int head_groups, row_groups;     // of a request: its items
   int tile, box_rows, box_shift, stages;   // keys per tile, keys per box (a power of two) and its log2, ring depth
   uint32_t plane_bytes, stage_bytes;   // of a tile's K (or V); of a ring stage
@@ -70,25 +70,23 @@ struct MhaParams {
   float scale_log2;                // softmax_scale * log2(e)
 };
 
-__device__ __forceinline__ void mma_16816_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// D (16 x 8) += A (16 x 16) B (16 x 8), both operands f16 or both bf16.
+template <bool F16>
+__device__ __forceinline__ void mma_16816(float2& c0, float2& c1, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c0.x), "+f"(c0.y), "+f"(c1.x), "+f"(c1.y)
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c0.x), "+f"(c0.y), "+f"(c1.x), "+f"(c1.y)
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_16816_bf16(float2 (&c)[2], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0].x), "+f"(c[0].y), "+f"(c[1].x), "+f"(c[1].y)
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_16816_f16(float2 (&c)[2], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0].x), "+f"(c[0].y), "+f"(c[1].x), "+f"(c[1].y)
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// Transposes an 8 x 8 matrix of 16-bit values held two to a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -109,16 +107,19 @@ __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t nthreads, bool v) 
       : "=r"(r) : "r"(id), "r"(nthreads), "r"(static_cast<uint32_t>(v)) : "memory");
   return r != 0;
 }
-__device__ __forceinline__ float quad_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+// Over the eight lanes that share lane % 4 (the keys of a column of scores).
+__device__ __forceinline__ float keys_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+__device__ __forceinline__ float keys_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
 }
 __device__ __forceinline__ float warp_max(float v) {   // v >= 0
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
-}
-__device__ __forceinline__ float quad_sum(float v) {
-  v += __shfl_xor_sync(0xffffffffu, v, 1);
-  return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
@@ -160,47 +161,56 @@ template <int D>
 __host__ __device__ constexpr uint32_t mha_merge_bytes() { return (MHA_WARPS / 2) * 16 * (D + 2) * 4; }
 constexpr uint32_t MHA_MISC_BYTES = 8 * 4 * MHA_MAX_STAGES + 4 * MHA_MAX_STAGES + 64 + 8 * (MHA_WARPS + 4) + 64;
 
-// One warp's state: 16 rows (thread: rows lane / 4 and lane / 4 + 8) of one kv head.
-template <int D, bool FP8>
+// One warp's state: 8 NR query rows of one kv head.  Both products are formed transposed, keys and dims as
+// the MMA's 16 rows, query rows as its 8 columns: S^T = K Q^T and O^T = V^T P^T, so that up to eight rows
+// (the usual group) waste nothing, where rows on the 16-side would be half padding in every score, weight
+// and register of O.  Thread (g, t) = (lane / 4, lane % 4) holds, of a group of 8 rows, rows 2t and 2t + 1.
+template <int D, bool FP8, int NR>
 struct MhaRows {
   static constexpr int CW = D * (FP8 ? 1 : 2) < 128 ? D * (FP8 ? 1 : 2) : 128;   // bytes of a column
-  uint32_t qa[D / 16][4];          // q as A fragments (bf16, or f16 times a power of two per row)
-  float o[D / 8][4];
-  float m[2];                      // reference maximum (base 2) of the thread's two rows
-  float2 l[2];                     // this thread's part of the sum (even, odd keys)
+  uint32_t qb[NR][D / 16][2];      // q as B fragments (bf16, or f16 times a power of two)
+  float2 o[D / 16][NR][2];         // O^T: dims A and B of a 16-dim block (dim_a, dim_b), rows 2t and 2t + 1
+  float m[NR][2];                  // reference maxima (base 2) of rows 2t, 2t + 1
+  float2 l[NR];                    // this thread's part of their sums
+  uint32_t last[NR][2];            // their last visible keys
   float xs;                        // score factor
-  uint32_t koff, voff;             // this lane's place in a 16-key block of K and V
-  uint32_t last[2];                // last visible key of each row
   float vref;                      // e4m3: power-of-two bound of V's scales so far (0: none yet)
+  uint32_t koff, voff;             // this lane's place in a 16-key block of K and V
 
   static __device__ __forceinline__ uint32_t swizzle(uint32_t r) { return CW == 128 ? (r & 7u) << 4 : ((r >> 1) & 3u) << 4; }
+  static __device__ __forceinline__ int dim_a(int k, int g) { return 16 * k + (FP8 ? 2 * g : g); }
+  static __device__ __forceinline__ int dim_b(int k, int g) { return 16 * k + (FP8 ? 2 * g + 1 : g + 8); }
 
-  // Query rows row0 .. row0 + 15 of kv head kvh (rows past the last one are zero).  For e4m3 caches q is
-  // brought to f16 by one power of two for the 16 rows (largest value into [2^12, 2^13)).
+  // Query rows row0 .. row0 + 8 NR - 1 of kv head kvh (rows past the last one are zero).  For e4m3 caches q
+  // is brought to f16 by one power of two for the warp's rows (largest value into [2^12, 2^13)).
   __device__ __forceinline__ void load_q(const MhaParams& p, int b, int kvh, int row0, int lane) {
-    const int t = lane & 3;
+    const int g = lane >> 2, t = lane & 3;
     uint32_t m2 = 0;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int r = row0 + (lane >> 2) + 8 * u;
+    for (int u = 0; u < NR; ++u) {
+      const int r = row0 + 8 * u + g;
       const bool have = r < p.R;
       const int i = have ? static_cast<int>(p.divG.div(r)) : 0;
       const int h = kvh * p.divG.d + (r - i * p.divG.d);
-      last[u] = mha_length(p, b) + i;
       const uint16_t* src = p.q + ((static_cast<size_t>(b) * p.T + i) * p.H + h) * D;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         if (!FP8) {
-          qa[k][u] = have ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * t) : 0u;
-          qa[k][u + 2] = have ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8 + 2 * t) : 0u;
+          qb[u][k][0] = have ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * t) : 0u;
+          qb[u][k][1] = have ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8 + 2 * t) : 0u;
         } else {
           const uint2 v = have ? *reinterpret_cast<const uint2*>(src + 16 * k + 4 * t) : make_uint2(0, 0);
-          qa[k][u] = v.x;
-          qa[k][u + 2] = v.y;
+          qb[u][k][0] = v.x;
+          qb[u][k][1] = v.y;
           m2 = __vmaxu2(__vmaxu2(m2, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
         }
       }
-      m[u] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int re = row0 + 8 * u + 2 * t + e;
+        last[u][e] = mha_length(p, b) + (re < p.R ? p.divG.div(re) : 0u);
+        m[u][e] = -INFINITY;
+      }
       l[u] = make_float2(0.f, 0.f);
     }
     xs = p.scale_log2;
@@ -210,41 +220,45 @@ struct MhaRows {
       const float f = pow2(e);
       xs = big >= 0x7F80u ? __uint_as_float(0x7FC00000u) : p.scale_log2 * pow2(-e);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
+      for (int u = 0; u < NR; ++u)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          qa[k][x] = ptx::pack_f16x2(__uint_as_float(qa[k][x] << 16) * f, __uint_as_float(qa[k][x] & 0xFFFF0000u) * f);
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            qb[u][k][x] = ptx::pack_f16x2(__uint_as_float(qb[u][k][x] << 16) * f, __uint_as_float(qb[u][k][x] & 0xFFFF0000u) * f);
     }
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
+    for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) o[n][x] = 0.f;
+      for (int u = 0; u < NR; ++u) o[k][u][0] = o[k][u][1] = make_float2(0.f, 0.f);
     vref = 0.f;
-    // ldmatrix rows and 16-byte units of this lane: K by keys (lane & 7) + 8 (lane / 16), V by keys lane & 15;
-    // a row's swizzle depends on the key's low bits only, which a step's multiple of 16 does not change
-    const uint32_t kr = (lane & 7) + ((lane >> 4) << 3), vr = lane & 15;
-    koff = kr * CW + ((((lane >> 3) & 1) * 16) ^ swizzle(kr));
-    voff = vr * CW + (((lane >> 4) * 16) ^ swizzle(vr));
+    // ldmatrix addresses of this lane: K as A fragments by key (lane & 15) and 16-byte half (lane / 16); V^T
+    // as A fragments, through transposing loads, by key (lane & 7) + 8 (lane / 16) and half (lane / 8) & 1.
+    // A row's swizzle depends on the key's low bits only, which a step's multiple of 16 does not change.
+    const uint32_t kr = lane & 15, vr = (lane & 7) + ((lane >> 4) << 3);
+    koff = kr * CW + (((lane >> 4) * 16) ^ swizzle(kr));
+    voff = vr * CW + ((((lane >> 3) & 1) * 16) ^ swizzle(vr));
   }
 
-  // A step takes 16 KS keys, at rows row .. of a page run.  KS = 2 halves the rescales and reductions per
-  // key and gives the MMAs four independent accumulators instead of two.
-  // Products q K^T: s[8-key group][row lane / 4: keys 2t, 2t + 1; row lane / 4 + 8: the same], t = lane % 4.
+  // A step takes 16 KS keys, at consecutive rows of a page run.
+  // Products: s[16-key block][row group][0: key g, 1: key g + 8] of rows 2t (x) and 2t + 1 (y).
   // kcol: the head's first column at the step's first row; pitch: bytes from column to column.
   template <int KS>
-  __device__ __forceinline__ void scores(uint32_t kcol, uint32_t pitch, float2 (&s)[2 * KS][2]) const {
+  __device__ __forceinline__ void scores(uint32_t kcol, uint32_t pitch, float2 (&s)[KS][NR][2]) const {
 #pragma unroll
-    for (int x = 0; x < 2 * KS; ++x) s[x][0] = s[x][1] = make_float2(0.f, 0.f);
+    for (int y = 0; y < KS; ++y)
+#pragma unroll
+      for (int u = 0; u < NR; ++u) s[y][u][0] = s[y][u][1] = make_float2(0.f, 0.f);
     const uint32_t a0 = kcol + koff, a1 = a0 + pitch;
     if (!FP8) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
 #pragma unroll
         for (int y = 0; y < KS; ++y) {
-          uint32_t kb[4];
-          ldsm4(((k * 32 < CW ? a0 : a1) ^ ((k * 32) % CW)) + y * 16 * CW, kb);
-          mma_16816_bf16(s[2 * y], qa[k], kb[0], kb[1]);
-          mma_16816_bf16(s[2 * y + 1], qa[k], kb[2], kb[3]);
+          uint32_t a[4];
+          ldsm4(((k * 32 < CW ? a0 : a1) ^ ((k * 32) % CW)) + y * 16 * CW, a);
+#pragma unroll
+          for (int u = 0; u < NR; ++u) mma_16816<false>(s[y][u][0], s[y][u][1], a, qb[u][k][0], qb[u][k][1]);
         }
     } else {
 #pragma unroll
@@ -254,132 +268,152 @@ struct MhaRows {
           uint32_t kb[4];
           ldsm4((a0 ^ (k * 16)) + y * 16 * CW, kb);
 #pragma unroll
-          for (int x = 0; x < 4; ++x)   // x & 1: k step, x >> 1: key half
-            mma_16816_f16(s[2 * y + (x >> 1)], qa[k + (x & 1)], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[x])),
-                          ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[x] >> 16)));
+          for (int x = 0; x < 2; ++x) {   // a lane's four consecutive dims are its two k pairs (q is permuted alike)
+            const uint32_t a[4] = {ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[2 * x])),
+                                   ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[2 * x + 1])),
+                                   ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[2 * x] >> 16)),
+                                   ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(kb[2 * x + 1] >> 16))};
+#pragma unroll
+            for (int u = 0; u < NR; ++u) mma_16816<true>(s[y][u][0], s[y][u][1], a, qb[u][k + x][0], qb[u][k + x][1]);
+          }
         }
     }
   }
 
-  // Scores to weights (pa: A fragments of the value product) against a reference maximum that trails the
+  // Scores to weights (pb: B fragments of the value product) against a reference maximum that trails the
   // running one by at most LAZY (log2): weights stay below 2^LAZY and O is rescaled rarely.  ks, vs: the
   // scales of the step's first key, sstep bytes from key to key; key0: the first key, n: stored keys.
   static constexpr float LAZY = 6.f;
   template <int KS>
-  __device__ __forceinline__ void weights(const MhaParams& p, float2 (&s)[2 * KS][2], uint32_t ks, uint32_t vs, uint32_t sstep,
-                                          uint32_t key0, uint32_t n, int lane, uint32_t (&pa)[KS][4]) {
-    const int t = lane & 3;
-    float2 sv[2 * KS];
+  __device__ __forceinline__ void weights(const MhaParams& p, float2 (&s)[KS][NR][2], uint32_t ks, uint32_t vs, uint32_t sstep,
+                                          uint32_t key0, uint32_t n, int lane, uint32_t (&pb)[KS][NR][2]) {
+    const int g = lane >> 2;
+    float sv[KS][2];
     if (FP8) {
-      ks += 2 * t * sstep;
-      vs += 2 * t * sstep;
+      ks += g * sstep;
+      vs += g * sstep;
     }
 #pragma unroll
-    for (int x = 0; x < 2 * KS; ++x) {  // keys 8 x + 2 t, + 1
-      float2 f = make_float2(xs, xs);
-      if (FP8) {
-        f = __fmul2_rn(make_float2(ptx::ld_shared_f32(ks), ptx::ld_shared_f32(ks + sstep)), f);
-        sv[x] = make_float2(ptx::ld_shared_f32(vs), ptx::ld_shared_f32(vs + sstep));
-        ks += 8 * sstep;
-        vs += 8 * sstep;
+    for (int y = 0; y < KS; ++y)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {     // key 16 y + 8 x + g
+        float f = xs;
+        if (FP8) {
+          f *= ptx::ld_shared_f32(ks);
+          sv[y][x] = ptx::ld_shared_f32(vs);
+          ks += 8 * sstep;
+          vs += 8 * sstep;
+        }
+#pragma unroll
+        for (int u = 0; u < NR; ++u) s[y][u][x] = __fmul2_rn(s[y][u][x], make_float2(f, f));
       }
-      s[x][0] = __fmul2_rn(s[x][0], f);
-      s[x][1] = __fmul2_rn(s[x][1], f);
-    }
     if (key0 + 16 * KS - 1 > n - p.T) {   // some row may not see some of the keys
 #pragma unroll
-      for (int x = 0; x < 2 * KS; ++x) {
-        const uint32_t key = key0 + 8 * x + 2 * t;
-        if (key > last[0]) s[x][0].x = -INFINITY;
-        if (key + 1 > last[0]) s[x][0].y = -INFINITY;
-        if (key > last[1]) s[x][1].x = -INFINITY;
-        if (key + 1 > last[1]) s[x][1].y = -INFINITY;
-        if (FP8 && key >= n) sv[x].x = 0.f;
-        if (FP8 && key + 1 >= n) sv[x].y = 0.f;
-      }
-    }
-    float m0 = s[0][0].x, m1 = s[0][1].x, top = 0.f;
+      for (int y = 0; y < KS; ++y)
 #pragma unroll
-    for (int x = 0; x < 2 * KS; ++x) {
-      m0 = fmaxf(m0, fmaxf(s[x][0].x, s[x][0].y));
-      m1 = fmaxf(m1, fmaxf(s[x][1].x, s[x][1].y));
-      if (FP8) top = fmaxf(top, fmaxf(fabsf(sv[x].x), fabsf(sv[x].y)));
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t key = key0 + 16 * y + 8 * x + g;
+#pragma unroll
+          for (int u = 0; u < NR; ++u) {
+            if (key > last[u][0]) s[y][u][x].x = -INFINITY;
+            if (key > last[u][1]) s[y][u][x].y = -INFINITY;
+          }
+          if (FP8 && key >= n) sv[y][x] = 0.f;
+        }
     }
-    // (the row's own lanes may disagree on whether a rescale is due: the vote decides for the warp)
-    if (__any_sync(0xffffffffu, m0 > m[0] + LAZY || m1 > m[1] + LAZY || (FP8 && top > vref))) {
-      m0 = fmaxf(m[0], quad_max(m0));
-      m1 = fmaxf(m[1], quad_max(m1));
+    float top = 0.f, mx[NR][2];
+    bool due = false;
+#pragma unroll
+    for (int u = 0; u < NR; ++u) {
+      mx[u][0] = s[0][u][0].x;
+      mx[u][1] = s[0][u][0].y;
+#pragma unroll
+      for (int y = 0; y < KS; ++y)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          mx[u][0] = fmaxf(mx[u][0], s[y][u][x].x);
+          mx[u][1] = fmaxf(mx[u][1], s[y][u][x].y);
+          if (FP8 && u == 0) top = fmaxf(top, fabsf(sv[y][x]));
+        }
+      due = due || mx[u][0] > m[u][0] + LAZY || mx[u][1] > m[u][1] + LAZY;
+    }
+    if (__any_sync(0xffffffffu, due || (FP8 && top > vref))) {
       float ref = vref;
       if (FP8) {
         top = warp_max(top);
         if (top > vref) ref = pow2(min(max(static_cast<int>(__float_as_uint(top) >> 23) - 126, -126), 126));
       }
-      // ex2(-inf) = 0; a row that has seen no key yet keeps -inf
-      const float c0 = m0 == -INFINITY ? 0.f : ptx::ex2_approx(m[0] - m0);
-      const float c1 = m1 == -INFINITY ? 0.f : ptx::ex2_approx(m[1] - m1);
       const float vc = FP8 && ref != vref ? vref / ref : 1.f;
-      l[0] = make_float2(l[0].x * c0, l[0].y * c0);
-      l[1] = make_float2(l[1].x * c1, l[1].y * c1);
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        o[k][0] *= c0 * vc;
-        o[k][1] *= c0 * vc;
-        o[k][2] *= c1 * vc;
-        o[k][3] *= c1 * vc;
-      }
-      m[0] = m0;
-      m[1] = m1;
       vref = ref;
+#pragma unroll
+      for (int u = 0; u < NR; ++u) {
+        const float m0 = fmaxf(m[u][0], keys_max(mx[u][0])), m1 = fmaxf(m[u][1], keys_max(mx[u][1]));
+        // ex2(-inf) = 0; a row that has seen no key yet keeps -inf
+        const float2 c = make_float2(m0 == -INFINITY ? 0.f : ptx::ex2_approx(m[u][0] - m0),
+                                     m1 == -INFINITY ? 0.f : ptx::ex2_approx(m[u][1] - m1));
+        l[u] = __fmul2_rn(l[u], c);
+        const float2 cv = __fmul2_rn(c, make_float2(vc, vc));
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          o[k][u][0] = __fmul2_rn(o[k][u][0], cv);
+          o[k][u][1] = __fmul2_rn(o[k][u][1], cv);
+        }
+        m[u][0] = m0;
+        m[u][1] = m1;
+      }
     }
-    const float r0 = m[0] == -INFINITY ? 0.f : -m[0], r1 = m[1] == -INFINITY ? 0.f : -m[1];
     // 1 / vref: a power of two's reciprocal has the mirrored exponent
     const float inv = FP8 && vref > 0.f ? __uint_as_float(0x7F000000u - __float_as_uint(vref)) : 0.f;
 #pragma unroll
-    for (int x = 0; x < 2 * KS; ++x) {
-      uint32_t* a = &pa[x >> 1][(x & 1) * 2];
+    for (int u = 0; u < NR; ++u) {
+      const float2 r = make_float2(m[u][0] == -INFINITY ? 0.f : -m[u][0], m[u][1] == -INFINITY ? 0.f : -m[u][1]);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float2 e = __fadd2_rn(s[x][u], u ? make_float2(r1, r1) : make_float2(r0, r0));
-        float2 w = make_float2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
-        l[u] = __fadd2_rn(l[u], w);
-        if (FP8) {
-          w = __fmul2_rn(w, __fmul2_rn(sv[x], make_float2(inv, inv)));
-          a[u] = ptx::pack_f16x2(w.x, w.y);
-        } else {
-          a[u] = ptx::pack_bf16x2(w.x, w.y);
+      for (int y = 0; y < KS; ++y)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float2 e = __fadd2_rn(s[y][u][x], r);
+          float2 w = make_float2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
+          l[u] = __fadd2_rn(l[u], w);
+          if (FP8) {
+            const float f = sv[y][x] * inv;
+            w = __fmul2_rn(w, make_float2(f, f));
+            pb[y][u][x] = transpose8(ptx::pack_f16x2(w.x, w.y));
+          } else {
+            pb[y][u][x] = transpose8(ptx::pack_bf16x2(w.x, w.y));
+          }
         }
-      }
     }
   }
 
-  // O += weights * V; vcol, pitch as for scores.
+  // O^T += V^T P^T; vcol, pitch as for scores.
   template <int KS>
-  __device__ __forceinline__ void values(uint32_t vcol, uint32_t pitch, const uint32_t (&pa)[KS][4]) {
+  __device__ __forceinline__ void values(uint32_t vcol, uint32_t pitch, const uint32_t (&pb)[KS][NR][2]) {
     const uint32_t a0 = vcol + voff, a1 = a0 + pitch;
     if (!FP8) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
 #pragma unroll
         for (int y = 0; y < KS; ++y) {
-          uint32_t vb[4];
-          ldsm4_t(((k * 32 < CW ? a0 : a1) ^ ((k * 32) % CW)) + y * 16 * CW, vb);
-          mma_16816_bf16(o[2 * k], pa[y], vb[0], vb[1]);
-          mma_16816_bf16(o[2 * k + 1], pa[y], vb[2], vb[3]);
+          uint32_t a[4];
+          ldsm4_t(((k * 32 < CW ? a0 : a1) ^ ((k * 32) % CW)) + y * 16 * CW, a);
+#pragma unroll
+          for (int u = 0; u < NR; ++u) mma_16816<false>(o[k][u][0], o[k][u][1], a, pb[y][u][0], pb[y][u][1]);
         }
     } else {
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k)          // 32 dims: two blocks of 16, an even and an odd tile each
+      for (int k = 0; k < D / 16; k += 2)       // 32 dims: two blocks of 16, whose even dims are A, odd dims B
 #pragma unroll
         for (int y = 0; y < KS; ++y) {
           uint32_t vb[4];
-          ldsm4_t((a0 ^ (k * 32)) + y * 16 * CW, vb);
+          ldsm4_t((a0 ^ (k * 16)) + y * 16 * CW, vb);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint32_t a = vb[2 * x], b = vb[2 * x + 1];
-            mma_16816_f16(o[4 * k + 2 * x], pa[y], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(a, 0, 0x4420))),
-                          ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(b, 0, 0x4420))));
-            mma_16816_f16(o[4 * k + 2 * x + 1], pa[y], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(a, 0, 0x4431))),
-                          ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(b, 0, 0x4431))));
+            const uint32_t a[4] = {ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(vb[x], 0, 0x4420))),
+                                   ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(vb[x], 0, 0x4431))),
+                                   ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(vb[x + 2], 0, 0x4420))),
+                                   ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(vb[x + 2], 0, 0x4431)))};
+#pragma unroll
+            for (int u = 0; u < NR; ++u) mma_16816<true>(o[k + x][u][0], o[k + x][u][1], a, pb[y][u][0], pb[y][u][1]);
           }
         }
     }
@@ -396,53 +430,57 @@ struct MhaRows {
     __syncwarp();
   }
 
-  // Adds another warp's state over other keys of the same rows (l already summed over the quad).
-  __device__ __forceinline__ void put(float* buf, int lane) const {
-    float* mine = buf + lane;
+  // The whole sums of the rows, and O in its own units.
+  __device__ __forceinline__ void finish_sums() {
 #pragma unroll
-    for (int k = 0; k < D / 8; ++k)
+    for (int u = 0; u < NR; ++u) {
+      l[u] = make_float2(keys_sum(l[u].x), keys_sum(l[u].y));
+      if (FP8)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) mine[(4 * k + x) * 32] = o[k][x];
-    if ((lane & 3) == 0) {
-      float* ml = buf + 16 * D + (lane >> 2) * 2;
-      ml[0] = m[0];
-      ml[1] = l[0].x;
-      ml[16] = m[1];
-      ml[17] = l[1].x;
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) o[k][u][x] = __fmul2_rn(o[k][u][x], make_float2(vref, vref));
     }
+  }
+  // Hands the state to, or takes it from, a warp with other keys of the same rows.
+  __device__ __forceinline__ void put(float* buf, int lane) const {
+    float2* mine = reinterpret_cast<float2*>(buf) + lane;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int u = 0; u < NR; ++u)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) mine[((k * NR + u) * 2 + x) * 32] = o[k][u][x];
+    if (lane < 4)
+#pragma unroll
+      for (int u = 0; u < NR; ++u)
+        reinterpret_cast<float4*>(buf + 16 * D)[u * 4 + lane] = make_float4(m[u][0], l[u].x, m[u][1], l[u].y);
   }
   __device__ __forceinline__ void add(const float* buf, int lane) {
-    const float* ml = buf + 16 * D + (lane >> 2) * 2;
-    float mine[2], theirs[2];
+    const float2* theirs = reinterpret_cast<const float2*>(buf) + lane;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float om = ml[16 * u], ol = ml[16 * u + 1], mm = fmaxf(m[u], om), ref = mm == -INFINITY ? 0.f : mm;
-      mine[u] = ptx::ex2_approx(m[u] - ref);
-      theirs[u] = ptx::ex2_approx(om - ref);
-      l[u].x = l[u].x * mine[u] + ol * theirs[u];
-      m[u] = mm;
-    }
+    for (int u = 0; u < NR; ++u) {
+      const float4 ml = reinterpret_cast<const float4*>(buf + 16 * D)[u * 4 + (lane & 3)];
+      const float m0 = fmaxf(m[u][0], ml.x), m1 = fmaxf(m[u][1], ml.z);
+      const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
+      const float2 a = make_float2(ptx::ex2_approx(m[u][0] - r0), ptx::ex2_approx(m[u][1] - r1));
+      const float2 c = make_float2(ptx::ex2_approx(ml.x - r0), ptx::ex2_approx(ml.z - r1));
+      l[u] = make_float2(l[u].x * a.x + ml.y * c.x, l[u].y * a.y + ml.w * c.y);
+      m[u][0] = m0;
+      m[u][1] = m1;
 #pragma unroll
-    for (int k = 0; k < D / 8; ++k)
+      for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        o[k][x] = o[k][x] * mine[x >> 1] + buf[lane + (4 * k + x) * 32] * theirs[x >> 1];
-  }
-  __device__ __forceinline__ void finish_sums() {
-    l[0].x = quad_sum(l[0].x + l[0].y);
-    l[1].x = quad_sum(l[1].x + l[1].y);
-    if (FP8) {
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[k][x] *= vref;
+        for (int x = 0; x < 2; ++x)
+          o[k][u][x] = __ffma2_rn(theirs[((k * NR + u) * 2 + x) * 32], c, __fmul2_rn(o[k][u][x], a));
     }
   }
 };
 
-template <int D, bool FP8, int KS>
+template <int D, bool FP8, int KS, int NR>
 __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __grid_constant__ MhaParams p) {
-  using Rows = MhaRows<D, FP8>;
+  using Rows = MhaRows<D, FP8, NR>;
+  constexpr int RT = 8 * NR;                             // rows of a warp
   constexpr int CPH = D * (FP8 ? 1 : 2) / Rows::CW;      // columns per head
   extern __shared__ uint8_t mha_smem_raw[];
   const uint32_t raw = ptx::smem_u32(mha_smem_raw);
@@ -599,7 +637,7 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
     int4 mine = make_int4(-1, 0, 0, 0);                  // the item this CTA holds the head of, if it is cut
     while (live && walk.next(p, u)) {
       const int hgi = u.item / p.row_groups, rgi = u.item - hgi * p.row_groups;
-      const int kvh = hgi * p.hg + hl, row0 = (rgi * p.mt + rt) * 16;
+      const int kvh = hgi * p.hg + hl, row0 = (rgi * p.mt + rt) * RT;
       const bool work = kvh < p.HKV && row0 < p.R;
       const uint32_t stored = mha_length(p, u.b) + p.T;
       w.load_q(p, u.b, work ? kvh : 0, work ? row0 : p.R, lane);
@@ -627,7 +665,7 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
       };
       const uint32_t g0 = kp * 16 * KS, gstep = p.kw * 16 * KS;
       uint32_t bad = 0;
-      float2 s[2 * KS][2];
+      float2 s[KS][NR][2];
       Step cur{};
       if (u.ta < u.tb) {
         if (!enter(stk, bad)) live = false;
@@ -639,8 +677,8 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
         for (uint32_t g = g0; g < static_cast<uint32_t>(p.tile) && live; g += gstep) {
           const bool end = g + gstep >= static_cast<uint32_t>(p.tile);   // this warp's last step of the tile
           const bool more = !end || j + 1 < u.tb;
-          uint32_t pa[KS][4];
-          if (cur.ok) w.template weights<KS>(p, s, cur.sc, cur.sc + vscales, sstep, cur.key0, stored, lane, pa);
+          uint32_t pb[KS][NR][2];
+          if (cur.ok) w.template weights<KS>(p, s, cur.sc, cur.sc + vscales, sstep, cur.key0, stored, lane, pb);
           if (end) {
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(empty_k(stk));   // the tile's K and scales are read
@@ -664,7 +702,7 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
             }
             // (the last step of a piece forms its own scores again: nothing reads them)
             w.template scores<KS>(nxt.k, pitch, s);
-            w.template values<KS>(v, pitch, pa);
+            w.template values<KS>(v, pitch, pb);
           } else if (nxt.ok) {
             w.template scores<KS>(nxt.k, pitch, s);
           }
@@ -700,43 +738,38 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
         mine = make_int4(u.b, u.item, static_cast<int>(c), 0);
       }
       if (work && kp == 0) {
+        const int gg = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int r = row0 + (lane >> 2) + 8 * v, t = lane & 3;
+        for (int v = 0; v < 2 * NR; ++v) {
+          const int x = v >> 1, e = v & 1, r = row0 + 8 * x + 2 * t + e;   // row group, row of the thread's two
           if (r >= p.R) continue;
-          const float inv = w.l[v].x > 0.f || w.l[v].x != w.l[v].x ? 1.f / w.l[v].x : 0.f;
-          const float lse2 = w.l[v].x > 0.f || w.l[v].x != w.l[v].x ? w.m[v] + log2f(w.l[v].x) : -INFINITY;
+          const float sum = e ? w.l[x].y : w.l[x].x;
+          const bool some = sum > 0.f || sum != sum;     // (a NaN is passed on)
+          const float inv = some ? 1.f / sum : 0.f, lse2 = some ? w.m[x][e] + log2f(sum) : -INFINITY;
           if (whole) {
             const int i = static_cast<int>(p.divG.div(r));
             const size_t row = (static_cast<size_t>(u.b) * p.T + i) * p.H + kvh * p.divG.d + (r - i * p.divG.d);
             uint16_t* out = p.out + row * D;
-            if (!FP8) {
 #pragma unroll
-              for (int k = 0; k < D / 8; ++k)
-                *reinterpret_cast<uint32_t*>(out + 8 * k + 2 * t) = ptx::pack_bf16x2(w.o[k][2 * v] * inv, w.o[k][2 * v + 1] * inv);
-            } else {
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k)
-                *reinterpret_cast<uint2*>(out + 16 * k + 4 * t) =
-                    make_uint2(ptx::pack_bf16x2(w.o[2 * k][2 * v] * inv, w.o[2 * k + 1][2 * v] * inv),
-                               ptx::pack_bf16x2(w.o[2 * k][2 * v + 1] * inv, w.o[2 * k + 1][2 * v + 1] * inv));
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t ab = ptx::pack_bf16x2((e ? w.o[k][x][0].y : w.o[k][x][0].x) * inv, (e ? w.o[k][x][1].y : w.o[k][x][1].x) * inv);
+              if (FP8) {
+                *reinterpret_cast<uint32_t*>(out + Rows::dim_a(k, gg)) = ab;   // dims 2g, 2g + 1
+              } else {
+                out[Rows::dim_a(k, gg)] = static_cast<uint16_t>(ab);
+                out[Rows::dim_b(k, gg)] = static_cast<uint16_t>(ab >> 16);
+              }
             }
-            if (p.lse && t == 0) p.lse[row] = lse2 * 0.6931471805599453f;
+            if (p.lse && gg == 0) p.lse[row] = lse2 * 0.6931471805599453f;
           } else {
-            const size_t row = (static_cast<size_t>(2 * blockIdx.x + (head ? 1 : 0)) * MHA_ROWS) + pair * 16 + (lane >> 2) + 8 * v;
+            const size_t row = (static_cast<size_t>(2 * blockIdx.x + (head ? 1 : 0)) * MHA_ROWS) + pair * RT + 8 * x + 2 * t + e;
             float* out = p.part_o + row * D;
-            if (!FP8) {
 #pragma unroll
-              for (int k = 0; k < D / 8; ++k)
-                *reinterpret_cast<float2*>(out + 8 * k + 2 * t) = make_float2(w.o[k][2 * v] * inv, w.o[k][2 * v + 1] * inv);
-            } else {
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k)
-                *reinterpret_cast<float4*>(out + 16 * k + 4 * t) =
-                    make_float4(w.o[2 * k][2 * v] * inv, w.o[2 * k + 1][2 * v] * inv,
-                                w.o[2 * k][2 * v + 1] * inv, w.o[2 * k + 1][2 * v + 1] * inv);
+            for (int k = 0; k < D / 16; ++k) {
+              out[Rows::dim_a(k, gg)] = (e ? w.o[k][x][0].y : w.o[k][x][0].x) * inv;
+              out[Rows::dim_b(k, gg)] = (e ? w.o[k][x][1].y : w.o[k][x][1].x) * inv;
             }
-            if (t == 0) p.part_lse[row] = lse2;
+            if (gg == 0) p.part_lse[row] = lse2;
           }
         }
       }
@@ -754,9 +787,9 @@ __global__ void __launch_bounds__(256) mla_mha_join_kernel(const __grid_constant
   const int4 d = p.desc[blockIdx.x];
   if (d.x < 0) return;
   const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int pair = row >> 4, hl = pair / p.mt, rt = pair - hl * p.mt;
+  const int pair = row / p.row_tile, hl = pair / p.mt, rt = pair - hl * p.mt;
   const int hgi = d.y / p.row_groups, rgi = d.y - hgi * p.row_groups;
-  const int kvh = hgi * p.hg + hl, r = (rgi * p.mt + rt) * 16 + (row & 15);
+  const int kvh = hgi * p.hg + hl, r = (rgi * p.mt + rt) * p.row_tile + row % p.row_tile;
   if (pair >= p.hg * p.mt || kvh >= p.HKV || r >= p.R) return;
   const int c0 = blockIdx.x, parts = d.z - c0 + 1;
   auto slot = [&](int k) { return (static_cast<size_t>(2 * (c0 + k) + (k == 0)) * MHA_ROWS) + row; };
