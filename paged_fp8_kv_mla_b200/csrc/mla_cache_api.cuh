@@ -225,19 +225,29 @@ mla_status_t mha_launch(const mla::MhaParams& p, const MhaPlan& m, cudaStream_t 
   return MLA_OK;
 }
 
-// Lanes per token: as many as its 16-byte chunks in one plane, in powers of two up to a warp.
+// Lanes per token: the largest power of two, up to a warp, that divides its 16-byte chunks in one plane;
+// chunks per lane at a time: as many as a lane has, up to four.
+template <int D, bool FP8, int LT>
+void mha_store_kernel(const mla::MhaStoreParams& p, cudaStream_t stream) {
+  auto* kernel = p.steps >= 3   ? mla::mla_mha_store_kernel<D, FP8, LT, 4>
+                 : p.steps == 2 ? mla::mla_mha_store_kernel<D, FP8, LT, 2> : mla::mla_mha_store_kernel<D, FP8, LT, 1>;
+  const uint64_t threads = static_cast<uint64_t>(p.tokens) * LT;
+  const dim3 grid(static_cast<unsigned>((threads + mla::MST_THREADS - 1) / mla::MST_THREADS), 2);
+  kernel<<<grid, mla::MST_THREADS, 0, stream>>>(p);
+}
+
 template <int D, bool FP8>
-mla_status_t mha_store_launch(const mla::MhaStoreParams& p, cudaStream_t stream) {
-  const int lanes = p.chunks >= 32 ? 32 : p.chunks >= 16 ? 16 : 8;
-  const uint64_t grid = (static_cast<uint64_t>(p.tokens) * lanes + mla::MST_THREADS - 1) / mla::MST_THREADS;
-  if (grid * mla::MST_THREADS > 0xFFFFFFFFull) return fail(MLA_ERR_UNSUPPORTED, "too many new tokens (%u)", p.tokens);
-  const dim3 g(static_cast<unsigned>(grid), 2);
+mla_status_t mha_store_launch(mla::MhaStoreParams& p, cudaStream_t stream) {
+  if (static_cast<uint64_t>(p.tokens) * 32 > 0xFFFFFFFFull - mla::MST_THREADS)
+    return fail(MLA_ERR_UNSUPPORTED, "too many new tokens (%u)", p.tokens);
+  const int chunks = p.HKV * D / 8, lanes = gcd_int(chunks, 32);
+  p.steps = chunks / lanes;
   if (lanes == 32)
-    mla::mla_mha_store_kernel<D, FP8, 32><<<g, mla::MST_THREADS, 0, stream>>>(p);
+    mha_store_kernel<D, FP8, 32>(p, stream);
   else if (lanes == 16)
-    mla::mla_mha_store_kernel<D, FP8, 16><<<g, mla::MST_THREADS, 0, stream>>>(p);
-  else if (D == 64)
-    mla::mla_mha_store_kernel<64, FP8, 8><<<g, mla::MST_THREADS, 0, stream>>>(p);
+    mha_store_kernel<D, FP8, 16>(p, stream);
+  else if (D == 64)                                      // an odd number of heads of 64 values
+    mha_store_kernel<64, FP8, 8>(p, stream);
   MLA_CUDA(cudaGetLastError());
   return MLA_OK;
 }
@@ -502,7 +512,6 @@ mla_status_t mla_mha_kv_store(const void* k, const void* v, const uint32_t* cach
   st = cache_device(&sms, &status);
   if (st != MLA_OK) return st;
   p.tokens = static_cast<unsigned int>(tokens);
-  p.chunks = s->num_kv_heads * s->head_dim / 8;
   p.k = static_cast<const uint16_t*>(k);
   p.v = static_cast<const uint16_t*>(v);
   p.cache_lengths = cache_lengths;

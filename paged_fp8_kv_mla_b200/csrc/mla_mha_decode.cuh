@@ -25,8 +25,8 @@
 // running power-of-two bound of V's scales so that f16 holds it with 11 bits.  The instructions of this
 // are what keeps an e4m3 cache from the copy rate: the loads alone run at it.
 //
-// Work split.  The tiles of all (request, head group, row group) items laid end to end are cut into
-// equal contiguous ranges, one per CTA.  An item cut by a range's end leaves normalised fp32 partials
+// Work split.  The tiles of all (request, head group, row group) items, with each item's fixed cost, laid
+// end to end are cut into equal contiguous ranges, one per CTA.  An item cut by a range's end leaves normalised fp32 partials
 // and their log-sum-exp in the workspace and a second kernel joins them; each CTA names the item whose
 // head it holds and the last CTA of it, so the join needs no plan and nothing has to start at zero.
 // Where all requests are short (one or two tiles), each CTA takes one item and the second launch is
@@ -131,27 +131,36 @@ __device__ __forceinline__ int mha_tiles(const MhaParams& p, int b) {   // of on
   return static_cast<int>((mha_length(p, b) + p.T + p.tile - 1) / p.tile);
 }
 
+// What an item costs beside its tiles (q, the epilogue), in tiles.  The ranges are cut by this cost: batches
+// of long and very short requests otherwise leave many short ones to a few CTAs (64 ragged requests, e4m3:
+// the last CTA ended at 102 us where the median ended at 79; 116 us a call with 0, 102 with 2, 97 with 4).
+constexpr int MHA_ITEM_COST = 4;
+
 // A CTA's piece of an item: tiles [ta, tb) of nt.
 struct MhaPiece {
   int b, item, ta, tb, nt;
 };
-// Walks the pieces of a CTA's range [r0, r1) of the items' tiles laid end to end.
+// Walks the pieces of a CTA's range of the items' costs laid end to end; the first MHA_ITEM_COST units of an
+// item hold no tile.  t0: the range's first unit within its first item, left: units left.
 struct MhaWalker {
   int b, item, t0;
   long long left;
   __device__ __forceinline__ bool next(const MhaParams& p, MhaPiece& u) {
-    if (left <= 0 || b >= p.B) return false;
-    u.b = b;
-    u.item = item;
-    u.nt = mha_tiles(p, b);
-    u.ta = t0;
-    u.tb = static_cast<int>(min(static_cast<long long>(u.nt), t0 + left));
-    left -= u.tb - u.ta;
-    t0 = 0;
-    if (++item == p.head_groups * p.row_groups) {
-      item = 0;
-      ++b;
-    }
+    do {
+      if (left <= 0 || b >= p.B) return false;
+      u.b = b;
+      u.item = item;
+      u.nt = mha_tiles(p, b);
+      const int end = static_cast<int>(min(static_cast<long long>(u.nt + MHA_ITEM_COST), t0 + left));
+      u.ta = max(t0 - MHA_ITEM_COST, 0);
+      u.tb = max(end - MHA_ITEM_COST, 0);
+      left -= end - t0;
+      t0 = 0;
+      if (++item == p.head_groups * p.row_groups) {
+        item = 0;
+        ++b;
+      }
+    } while (u.ta == u.tb);
     return true;
   }
 };
@@ -520,11 +529,11 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
       start[1] = blockIdx.x - start[0] * items;
       start[2] = 0;
     }
-    r1 = mha_tiles(p, blockIdx.x / items);
+    r1 = mha_tiles(p, blockIdx.x / items) + MHA_ITEM_COST;
     __syncthreads();
   } else {
     long long mine = 0;
-    for (int b = threadIdx.x; b < p.B; b += MHA_THREADS) mine += static_cast<long long>(mha_tiles(p, b)) * items;
+    for (int b = threadIdx.x; b < p.B; b += MHA_THREADS) mine += static_cast<long long>(mha_tiles(p, b) + MHA_ITEM_COST) * items;
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane == 0) tot[warp] = mine;
     __syncthreads();
@@ -536,8 +545,8 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
     long long before = 0;
     for (int b0 = 0; b0 < p.B && before <= r0; b0 += MHA_THREADS) {
       const int b = b0 + threadIdx.x;
-      const int nt = b < p.B ? mha_tiles(p, b) : 0;
-      const long long n = static_cast<long long>(nt) * items;
+      const int cost = b < p.B ? mha_tiles(p, b) + MHA_ITEM_COST : 0;
+      const long long n = static_cast<long long>(cost) * items;
       long long inc = n;
       for (int o = 1; o < 32; o <<= 1) {
         const long long up = __shfl_up_sync(0xffffffffu, inc, o);
@@ -550,8 +559,8 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
       if (off + inc - n <= r0 && r0 < off + inc) {
         const long long in = r0 - (off + inc - n);
         start[0] = b;
-        start[1] = static_cast<int>(in / nt);
-        start[2] = static_cast<int>(in % nt);
+        start[1] = static_cast<int>(in / cost);
+        start[2] = static_cast<int>(in % cost);
       }
       for (int w = 0; w < MHA_THREADS / 32; ++w) before += tot[w];
       __syncthreads();

@@ -196,6 +196,20 @@ def test_store_is_exact(lengths, T, HKV, D, page, kw, fp8):
         assert torch.equal(ds.cpu().view(torch.int32), scales.view(torch.int32))
 
 
+def test_store_scale_of_every_bf16_maximum():
+    """amax / 448 rounds like the IEEE quotient for every positive finite bf16 value."""
+    top = torch.arange(1, 0x7F80, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    n = top.numel()
+    cache = MhaCache([n], 64, 1, 64, True, seed=34)
+    k = torch.zeros((1, n, 1, 64), dtype=torch.bfloat16)
+    k[0, :, 0, 17] = -top
+    db, ds, table, _ = cache.cuda()
+    M.mha_kv_store(k.cuda(), k.cuda(), torch.tensor([0], dtype=torch.int32).cuda(), table, None, 0, db, ds)
+    assert M.device_status() == 0
+    blk, slot = rows_of(cache.table, 0, n, 64)
+    assert torch.equal(ds.cpu()[blk, 0, 0, slot, 0, 0], top.float() / 448.0)
+
+
 def test_store_bad_page_is_skipped_and_flagged():
     cache = MhaCache([20, 20], 16, 2, 64, True, seed=33)
     db, ds, table, _ = cache.cuda()
