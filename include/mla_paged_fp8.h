@@ -344,7 +344,8 @@ mla_status_t mla_merge_lse_parts_bf16(const void* outs, const float* lses, int32
  *                 MLA_ERR_UNSUPPORTED)
  *   lse           fp32 [batch, max_prompt_length, num_q_heads], natural log, read
  *   scores        fp32, row b at scores + b * scores_stride; may be NULL (all zero)
- *   out           fp32, row b at out + b * out_stride; may be scores itself (same stride)
+ *   out           fp32, row b at out + b * out_stride; may be scores itself (same stride), else no row of
+ *                 out may overlap a row of scores
  *   workspace     device memory of at least mla_accumulate_workspace_bytes bytes, 16-byte aligned, for
  *                 the split q.  It is the caller's: calls that overlap on the device, or captured graphs
  *                 that are replayed at the same time, need one each.  Nothing in it has to start at zero
@@ -376,7 +377,7 @@ mla_status_t mla_accumulate_workspace_bytes(uint32_t max_prompt_length, const ml
  *                 clamped to it and flagged, MLA_ERR_DEVICE_BOUNDS)
  *   budget        >= 1; num_recent, num_sink >= 0 with num_recent + num_sink <= budget
  *   kept          int32, row b at kept + b * kept_stride (kept_stride >= min(budget, max_length))
- *   kept_lengths  int32 [batch], written
+ *   kept_lengths  int32 [batch], written; may be lengths itself
  * No workspace; batch = 0 is a no-op.
  */
 mla_status_t mla_select_keys(
@@ -393,7 +394,7 @@ mla_status_t mla_select_keys(
  *   kept, kept_lengths    int32; row b at kept + b * kept_stride, at most max_kept entries read
  *   lookup_table, scales_lookup_table, layer_idx   as for mla_decode_paged_fp8
  *   element_bytes         1 (e4m3 codes) or 2 (bf16) per element of blocks
- *   shape                 batch, num_blocks, kv_dim, num_layers, page_size (any), num_kv_heads,
+ *   shape                 batch (at most 65535), num_blocks, kv_dim, num_layers, page_size (any), num_kv_heads,
  *                         head_dim, num_scale_blocks, head_dim_granularity (any) and max_pages; a
  *                         token's row, num_kv_heads * head_dim * element_bytes, is a multiple of 32
  *   blocks                16-byte aligned; scales fp32 or NULL (none); both written in place
@@ -437,7 +438,7 @@ mla_status_t mla_mha_kv_store(
  * stored tokens are to be finite; what the cache holds behind a request's end is never used.
  *
  *   q          bf16 [batch, max_prompt_length, num_q_heads, head_dim], 16-byte aligned
- *   out        bf16, as q; lse fp32 [batch, max_prompt_length, num_q_heads], natural log, or NULL
+ *   out        bf16, as q, not overlapping it; lse fp32 [batch, max_prompt_length, num_q_heads], natural log, or NULL
  *   workspace  device memory of at least mla_mha_decode_workspace_bytes bytes (0 for short caches:
  *              then NULL may be passed), 16-byte aligned, for the partial results of requests that are
  *              split over SMs.  It is the caller's: calls that overlap on the device, or captured
@@ -477,7 +478,8 @@ mla_status_t mla_set_timing_events(cudaEvent_t before, cudaEvent_t after);
 
 /*
  * mla_set_wait_limit_ns -- bound of every wait inside the decode kernel (the roles of a CTA pair
- * hand tiles to each other through mbarriers).  A wait that runs out makes every role of the pair
+ * hand tiles to each other through mbarriers), and inside the kernels of
+ * mla_accumulate_weights_fp8 and mla_mha_decode_paged.  A wait that runs out makes every role of the pair
  * stop, drain its own copies and MMAs and return; the call's results are then undefined and the
  * next mla_get_device_status returns MLA_ERR_TIMEOUT.  Default 2 s; accepted range [1 ms, 60 s]
  * (else MLA_ERR_INVALID_ARG).  Process-wide; applies to calls made after it.

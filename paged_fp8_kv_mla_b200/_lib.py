@@ -382,6 +382,16 @@ def _rows(name, t, dtype, batch, cols):
     return step
 
 
+def _apart(name, t, tstep, other, u, ustep, cols):
+    """Refuses two row buffers that overlap in part (columns of one wide buffer may interleave)."""
+    a, b, size = t.data_ptr(), u.data_ptr(), 4 * cols
+    if a + 4 * ((t.shape[0] - 1) * tstep + cols) <= b or b + 4 * ((u.shape[0] - 1) * ustep + cols) <= a:
+        return
+    if tstep == ustep and size <= (b - a) % (4 * tstep) <= 4 * tstep - size:
+        return
+    raise ValueError(f"{name} must be {other} itself or not overlap it")
+
+
 def _one_device(first, *rest):
     """Index of the one CUDA device that all tensors are on."""
     d = first.get_device()
@@ -494,6 +504,10 @@ def accumulate_weights(q, lse, blocks, scales, cache_lengths, lookup_table, scal
             ostep = need
         else:
             out, ostep = scores, sstep
+    elif scores is not None and (out.data_ptr() != scores.data_ptr() or ostep != sstep):
+        _apart("out", out, ostep, "scores", scores, sstep, need)
+    if B == 0:
+        return out
     if workspace is None:
         workspace = _scratch(accumulate_workspace_bytes(B, T, H), q, dev, stream)
     _run(dev, lib.mla_accumulate_weights_fp8, q.data_ptr(), lse.data_ptr(), blocks.data_ptr(), scales.data_ptr(),
@@ -518,7 +532,7 @@ def select_keys(scores, lengths, max_length: int, budget: int, num_recent: int =
     scores fp32 [B, >= max_length] (rows may be strided), lengths int32 [B] keys held, max_length >= all of
     them.  A request over the budget keeps its first num_sink keys, its last num_recent keys and the
     keys with the largest scores between (ties to the lowest index); kept[b, :kept_lengths[b]] ascends
-    and later entries are left as they were (0 in a new tensor).
+    and later entries are left as they were (0 in a new tensor).  kept_lengths may be lengths itself.
     """
     if not _plain(lengths, _I32, 1):
         _expect("lengths", lengths, _U32, ndim=1)
@@ -536,6 +550,8 @@ def select_keys(scores, lengths, max_length: int, budget: int, num_recent: int =
                 kept = torch.zeros((B, kstep), dtype=_I32, device=scores.device)
             if kept_lengths is None:
                 kept_lengths = torch.empty(B, dtype=_I32, device=scores.device)
+    if B == 0:
+        return kept, kept_lengths
     _run(dev, lib.mla_select_keys, scores.data_ptr(), sstep, lengths.data_ptr(), B, int(max_length), int(budget),
          int(num_recent), int(num_sink), kept.data_ptr(), kstep, kept_lengths.data_ptr(), _raw_stream(stream, dev))
     return kept, kept_lengths
@@ -569,6 +585,8 @@ def compact_cache(kept, kept_lengths, lookup_table, scales_lookup_table, layer_i
             raise ValueError("without a scales_lookup_table, scales must have as many blocks as blocks")
     sstep = 0 if scores is None else _rows("scores", scores, _F32, B, 1)
     dev = _one_device(kept, kept_lengths, lookup_table, scales_lookup_table, blocks, scales, scores)
+    if B == 0:
+        return blocks, scales, scores
     shp = PagedShape(B, 0, D, 0, NB, KVD, NL, P, NKV, NSB, g, lookup_table.shape[1])
     _run(dev, load().mla_compact_paged, kept.data_ptr(), kstep, kept.shape[1], kept_lengths.data_ptr(),
          lookup_table.data_ptr(), _adr(scales_lookup_table), int(layer_idx), blocks.element_size(), ctypes.byref(shp),
@@ -613,6 +631,8 @@ def mha_kv_store(k, v, cache_lengths, lookup_table, scales_lookup_table, layer_i
         raise ValueError("k and v must have the same shape")
     shp = _check_mha(blocks, scales, cache_lengths, lookup_table, scales_lookup_table, B, 0, HKV, D)
     dev = _one_device(k, v, blocks, scales, cache_lengths, lookup_table, scales_lookup_table)
+    if B == 0 or T == 0:
+        return blocks, scales
     _run(dev, load().mla_mha_kv_store, k.data_ptr(), v.data_ptr(), cache_lengths.data_ptr(), lookup_table.data_ptr(),
          _adr(scales_lookup_table), T, int(layer_idx), blocks.element_size(), ctypes.byref(shp), blocks.data_ptr(), _adr(scales),
          _raw_stream(stream, dev))
@@ -647,6 +667,8 @@ def mha_decode(q, blocks, scales, cache_lengths, lookup_table, scales_lookup_tab
                 out = torch.empty_like(q)
             if lse is None and want_lse:
                 lse = torch.empty((B, T, H), dtype=_F32, device=q.device)
+    if B == 0:
+        return out, lse
     if workspace is None:
         workspace = _scratch(_mha_workspace(dev, T, int(max_cache_length), blocks.element_size(), B, H, D, shp.num_kv_heads,
                                             shp.page_size, shp.max_pages), q, dev, stream)

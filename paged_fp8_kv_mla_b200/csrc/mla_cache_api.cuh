@@ -279,6 +279,8 @@ mla_status_t mla_accumulate_weights_fp8(const void* q, const float* lse, const v
   if (out_stride < need || (scores && scores_stride < need))
     return fail(MLA_ERR_INVALID_ARG, "the rows of scores and out must hold max_cache_length + max_prompt_length = %lld values",
                 static_cast<long long>(need));
+  if (scores == out && scores_stride != out_stride)
+    return fail(MLA_ERR_INVALID_ARG, "out may be scores only with the same stride");
   if (d.B == 0) return MLA_OK;
   if (static_cast<int64_t>(d.T) * d.G > 0x3FFFFFFF) return fail(MLA_ERR_UNSUPPORTED, "too many query tokens");
   int sms = 0;
@@ -371,7 +373,7 @@ mla_status_t mla_select_keys(const float* scores, int64_t scores_stride, const u
   if (budget < 1) return fail(MLA_ERR_INVALID_ARG, "budget must be >= 1");
   if (static_cast<int64_t>(num_recent) + num_sink > budget)
     return fail(MLA_ERR_INVALID_ARG, "num_recent %d + num_sink %d exceed the budget %d", num_recent, num_sink, budget);
-  if (!scores || !lengths || !kept || !kept_lengths)
+  if (!lengths || !kept_lengths || (max_length > 0 && (!scores || !kept)))
     return fail(MLA_ERR_INVALID_ARG, "scores, lengths, kept and kept_lengths must be non-NULL");
   if (!aligned4(scores) || !aligned4(kept)) return fail(MLA_ERR_INVALID_ARG, "scores and kept must be 4-byte aligned");
   if (max_length >= (1u << 30)) return fail(MLA_ERR_UNSUPPORTED, "max_length too large");
@@ -568,6 +570,7 @@ mla_status_t mla_mha_decode_paged(const void* q, const void* blocks, const float
   if (!(softmax_scale == softmax_scale)) return fail(MLA_ERR_INVALID_ARG, "softmax_scale is NaN");
   MhaPlan m{};
   if (s->batch == 0) return mha_plan(s, max_prompt_length, max_cache_length, element_bytes, 1, &m);
+  if (q == out) return fail(MLA_ERR_INVALID_ARG, "out must not be q");
   int sms = 0;
   unsigned int* status = nullptr;
   st = cache_device(&sms, &status);

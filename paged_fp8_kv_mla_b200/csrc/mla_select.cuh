@@ -81,6 +81,8 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) mla_select_kernel(const __grid
   const uint32_t n = min(given, p.max_length);
   const uint32_t count = min(n, static_cast<uint32_t>(p.budget));
   int32_t* out = p.kept + b * p.kept_stride;
+  // kept_lengths may be lengths: it is written once every CTA of the cluster has read the length
+  ptx::cluster_sync();
   if (rank == 0 && tid == 0) {
     if (given > p.max_length) raise_status(p.status, STATUS_BOUNDS);
     p.kept_lengths[b] = static_cast<int32_t>(count);

@@ -218,3 +218,50 @@ def test_graph_capture_and_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     check(out, want, tol, torch.full(scores.shape, -7.0))
+
+
+def test_a_step_of_many_tokens_runs_in_several_launches():
+    """More split query tokens than the workspace holds at once (256 MB): the sums carry on from launch to
+    launch.  64-bit sums on the GPU."""
+    lengths, T, H = [40, 0, 130, 300, 7, 260, 90, 129], 300, 128
+    assert M.accumulate_workspace_bytes(8, T, H) < 8 * T * H * (2 * 576 + 8)
+    cache, q, scores = make(lengths, T, H, 64, seed=13)
+    blocks, scales, table, stable = cache.cuda()
+    lse = torch.empty((8, T, H)).cuda()
+    want, tol = torch.zeros(scores.shape).double(), torch.zeros(scores.shape).double()
+    for b, L in enumerate(lengths):
+        k, qq = cache.keys(b, L + T).cuda(), q[b].double().cuda()
+        x = torch.einsum("thd,kd->thk", qq, k) * SCALE
+        late = torch.arange(L + T, device="cuda")[None] > L + torch.arange(T, device="cuda")[:, None]
+        x = x.masked_fill(late[:, None], float("-inf"))
+        lse[b] = x.logsumexp(-1)
+        w = torch.exp(x - lse[b].double()[..., None])
+        amp = torch.einsum("thd,kd->thk", qq.abs(), k.abs()) * SCALE
+        rel = 584 * U * amp + 8 * U * (x.masked_fill(late[:, None], 0).abs() + lse[b].abs()[..., None]) + 2.0 ** -20
+        rel = rel + qq.abs().amax(-1)[..., None] * k.abs().sum(-1) * SCALE * 2.0 ** -17
+        want[b, :L + T] = w.sum((0, 1)).cpu()
+        want[b, :L] += scores[b, :L].double()
+        tol[b, :L + T] = (w * rel).sum((0, 1)).cpu() + (T * H + 2) * U * want[b, :L + T] + T * H * 2.0 ** -126
+    got = M.accumulate_weights(q.cuda(), lse, blocks, scales, torch.tensor(lengths, dtype=torch.int32).cuda(), table, stable, T,
+                               max(lengths), 0, SCALE, scores.cuda(), out=torch.zeros(scores.shape).cuda()).cpu().double()
+    assert M.device_status() == 0
+    assert ((got - want).abs() <= tol).all()
+
+
+def test_out_beside_scores_and_overlaps_refused():
+    """out and scores as column ranges of one buffer; a partial overlap is refused, an empty batch is fine."""
+    lengths = [50, 20]
+    cache, q, scores = make(lengths, 1, 8, 16, seed=14)
+    lse, want, tol = reference(cache, q, scores, lengths)
+    wide = torch.zeros((2, 110)).cuda()
+    wide[:, :51] = scores.cuda()
+    wide[:, 51:] = -7.0
+    run(cache, q, lse, lengths, wide[:, :51], out=wide[:, 51:102])
+    check(wide[:, 51:102], want, tol, torch.full((2, 51), -7.0))
+    assert torch.equal(wide[:, :51].cpu(), scores) and (wide[:, 102:] == -7.0).all()
+    with pytest.raises(ValueError, match="overlap"):
+        run(cache, q, lse, lengths, wide[:, :51], out=wide[:, 30:81])
+    blocks, scales, table, stable = cache.cuda()
+    none = M.accumulate_weights(q[:0].cuda(), lse[:0].cuda(), blocks, scales, torch.zeros(0, dtype=torch.int32).cuda(), table[:0],
+                                stable, 1, 50, 0, SCALE)
+    assert none.shape == (0, 51)

@@ -164,6 +164,21 @@ def test_decode_two_streams_and_a_graph():
         check(cases[i][0], new[i], lengths, 0.09, outs[i][0], outs[i][1])
 
 
+def test_decode_refuses_out_on_q_and_takes_an_empty_batch():
+    cache, q = make([30, 40], 1, 8, 2, 64, 16, False, seed=41)
+    blocks, scales, table, stable = cache.cuda()
+    lens, qd = torch.tensor([30, 40], dtype=torch.int32).cuda(), q.cuda()
+    with pytest.raises(M.MlaError, match="out must not be q"):
+        M.mha_decode(qd, blocks, scales, lens, table, stable, 1, 40, 0, 0.1, out=qd)
+    out, lse = M.mha_decode(qd[:0], blocks, scales, lens[:0], table[:0], stable, 1, 40, 0, 0.1)
+    assert out.shape == (0, 1, 8, 64) and lse.shape == (0, 1, 8)
+    with pytest.raises(M.MlaError, match="workspace"):
+        big, bq = make([3000], 1, 8, 2, 64, 16, False, seed=42)
+        b = big.cuda()
+        M.mha_decode(bq.cuda(), b[0], None, torch.tensor([3000], dtype=torch.int32).cuda(), b[2], None, 1, 3000, 0, 0.1,
+                     workspace=torch.empty(64, dtype=torch.uint8).cuda())
+
+
 @pytest.mark.parametrize("lengths,T,HKV,D,page,kw", [
     ([0], 1, 1, 64, 16, {}), ([5, 0, 30], 1, 8, 128, 16, {}), ([10, 100], 37, 3, 64, 48, dict(layers=2, layer=1)),
     ([63, 1], 200, 5, 128, 64, dict(own_scale_pages=True)),

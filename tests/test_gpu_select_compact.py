@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import paged_fp8_kv_mla_b200 as M
-from tests.cache_ref import LatentCache, MhaCache, page_table, rows_of, select_reference
+from tests.cache_ref import LatentCache, MhaCache, rows_of, select_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -73,10 +73,23 @@ def test_select_strided_rows_many_requests_and_a_long_length():
         assert whole[b, 10:10 + len(want)].tolist() == want and int(count[b]) == len(want)
 
 
-def moved(store, table, stable_or_table, b, kept, page, layer):
-    """The rows that request b's first len(kept) positions hold after the move."""
-    blk, slot = rows_of(table, b, max(kept) + 1, page)
-    return store[blk[kept], :, layer, slot[kept]]
+@pytest.mark.parametrize("top", [300, 5000, 70000])
+def test_select_writes_the_lengths_in_place(top):
+    """kept_lengths may be lengths itself, for clusters of every size; a batch of nothing is fine."""
+    lengths = [top, 5, top // 2, top - 1]
+    x = weights(4, top, 9, "plain")
+    lens = torch.tensor(lengths, dtype=torch.int32).cuda()
+    for _ in range(3):
+        now = lens.clone()
+        kept, same = M.select_keys(x.cuda(), now, top, 100, 10, 2, kept_lengths=now)
+        assert same is now and M.device_status() == 0
+        for b, n in enumerate(lengths):
+            want = select_reference(x[b].tolist(), n, 100, 10, 2)
+            assert kept[b, :int(now[b])].tolist() == want
+    kept, count = M.select_keys(x.cuda()[:0], lens[:0], top, 100)
+    assert kept.shape == (0, 100) and count.shape == (0,)
+    kept, count = M.select_keys(torch.zeros((2, 0)).cuda(), torch.zeros(2, dtype=torch.int32).cuda(), 0, 8)
+    assert count.tolist() == [0, 0] and M.device_status() == 0
 
 
 def check_compact(cache, kept, scores, **call):
