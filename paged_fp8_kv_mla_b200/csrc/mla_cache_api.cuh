@@ -21,6 +21,10 @@ cudaError_t mha_smem() {
   if (e == cudaSuccess) e = set(mla::mla_mha_decode_kernel<D, FP8, 2, 1>);
   if (e == cudaSuccess) e = set(mla::mla_mha_decode_kernel<D, FP8, 1, 2>);
   if (e == cudaSuccess) e = set(mla::mla_mha_decode_kernel<D, FP8, 2, 2>);
+  if constexpr (D == 64 && FP8) {
+    if (e == cudaSuccess) e = set(mla::mla_mha_decode_kernel<64, true, 4, 1>);
+    if (e == cudaSuccess) e = set(mla::mla_mha_decode_kernel<64, true, 4, 2>);
+  }
   return e;
 }
 
@@ -173,11 +177,13 @@ mla_status_t mha_plan(const mla_paged_shape_t* s, uint32_t T, uint32_t max_cache
   m.kw = 1;
   while (2 * m.kw * m.hg * m.mt <= mla::MHA_WARPS) m.kw *= 2;
   // Tile: 32 keys per warp at a time where a run of pages holds them and a ring stage of them takes at most
-  // 72 KB (three stages), else 16; doubled while a stage stays within 32 KB.
+  // 72 KB (three stages), else 16; doubled while a stage stays within 72 KB (two steps per hand-over).  e4m3
+  // heads of 64 take 64 keys at a time (128 x 8k, 8 kv heads: 194 us, 215 with 32, 244 in tiles of 32).
   const uint32_t per_key = 2u * m.hg * s->head_dim * element_bytes + (element_bytes == 1 ? 8u * s->num_kv_heads : 0u);
   m.ks = s->page_size % 32 == 0 && 32 * m.kw * per_key <= 73728 ? 2 : 1;
+  if (s->head_dim == 64 && element_bytes == 1 && s->page_size % 64 == 0 && 64 * m.kw * per_key <= 73728) m.ks = 4;
   m.tile = 16 * m.ks * m.kw;
-  while (m.tile < 128 && 2 * m.tile * per_key <= 32768) m.tile *= 2;
+  while (m.tile < 128 && 2 * m.tile * per_key <= 73728) m.tile *= 2;
   m.box_rows = gcd_int(s->page_size, m.tile);
   m.plane_bytes = static_cast<uint32_t>(m.tile) * m.hg * s->head_dim * element_bytes;
   m.stage_bytes = static_cast<uint32_t>(align_up(m.tile * per_key, 1024));
@@ -209,6 +215,8 @@ template <int D, bool FP8>
 mla_status_t mha_launch(const mla::MhaParams& p, const MhaPlan& m, cudaStream_t stream) {
   auto* kernel = m.nr == 1 ? (m.ks == 2 ? mla::mla_mha_decode_kernel<D, FP8, 2, 1> : mla::mla_mha_decode_kernel<D, FP8, 1, 1>)
                            : (m.ks == 2 ? mla::mla_mha_decode_kernel<D, FP8, 2, 2> : mla::mla_mha_decode_kernel<D, FP8, 1, 2>);
+  if constexpr (D == 64 && FP8)
+    if (m.ks == 4) kernel = m.nr == 1 ? mla::mla_mha_decode_kernel<64, true, 4, 1> : mla::mla_mha_decode_kernel<64, true, 4, 2>;
   kernel<<<m.NC, mla::MHA_THREADS, m.smem, stream>>>(p);
   MLA_CUDA(cudaGetLastError());
   if (m.one_item) return MLA_OK;
