@@ -45,6 +45,9 @@ mla_status_t cache_device(int* sms, unsigned int** status) {
     MLA_CUDA(smem(mla::mla_accumulate_kernel, mla::ACC_SMEM_ALLOC));
     MLA_CUDA(smem(mla::mla_select_kernel<512>, mla::SEL_KEYS_OFF + mla::SEL_CACHE * 4));
     MLA_CUDA(smem(mla::mla_select_kernel<1024>, mla::SEL_KEYS_OFF + mla::SEL_CACHE * 4));
+    MLA_CUDA(smem(mla::mla_compact_kernel<64, 256, 4, 3, 3>, 3 * 4 * 256 * mla::CMP_SLOT));
+    MLA_CUDA(smem(mla::mla_compact_kernel<32, 512, 2, 4, 2>, 4 * 2 * 512 * mla::CMP_SLOT));
+    MLA_CUDA(smem(mla::mla_compact_kernel<32, 1024, 2, 5, 1>, 5 * 2 * 1024 * mla::CMP_SLOT));
     MLA_CUDA((mha_smem<64, false>()));
     MLA_CUDA((mha_smem<64, true>()));
     MLA_CUDA((mha_smem<128, false>()));
@@ -231,6 +234,15 @@ mla_status_t mha_launch(const mla::MhaParams& p, const MhaPlan& m, cudaStream_t 
   cfg.numAttrs = 1;
   MLA_CUDA(cudaLaunchKernelEx(&cfg, mla::mla_mha_join_kernel<D>, p));
   return MLA_OK;
+}
+
+// A compaction kernel: slices, threads, rows per lane and chunk, chunks in shared memory, CTAs per SM.
+template <int SLICE, int THREADS, int U, int S, int CTAS>
+constexpr size_t compact_smem() { return static_cast<size_t>(S) * U * THREADS * mla::CMP_SLOT; }
+template <int SLICE, int THREADS, int U, int S, int CTAS>
+void compact_launch(const mla::CompactParams& p, dim3 grid, cudaStream_t stream) {
+  mla::mla_compact_kernel<SLICE, THREADS, U, S, CTAS>
+      <<<grid, THREADS, compact_smem<SLICE, THREADS, U, S, CTAS>(), stream>>>(p);
 }
 
 // Lanes per token: the largest power of two, up to a warp, that divides its 16-byte chunks in one plane;
@@ -487,8 +499,8 @@ mla_status_t mla_compact_paged(const int32_t* kept, int64_t kept_stride, int32_t
   p.divP = make_fastdiv(static_cast<uint32_t>(s->page_size));
   p.divW = make_fastdiv(static_cast<uint32_t>(row_words));
   // Slices of 64 bytes where they give every SM a CTA, else of 32 bytes; those in CTAs of 512 threads where
-  // there are more of them than SMs, else of 1024.  (12 requests of 30k: 63 us with 512, 71 with 1024;
-  // 4 of 128k: 192 and 146.)
+  // there are more of them than SMs, else of 1024.  (12 requests of 30k cut to 15k: 57 us; 4 of 128k to 64k:
+  // 116, 167 with 64-byte slices, of which there are 36.)
   const int64_t planes = static_cast<int64_t>(s->batch) * s->kv_dim;
   const bool narrow = row_bytes % 64 != 0 || planes * (row_bytes / 64) < sms;
   p.slices = static_cast<int>(row_bytes / (narrow ? 32 : 64));
@@ -496,11 +508,11 @@ mla_status_t mla_compact_paged(const int32_t* kept, int64_t kept_stride, int32_t
   if (gx > 0x7FFFFFFF) return fail(MLA_ERR_UNSUPPORTED, "grid too large");
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(s->batch));
   if (!narrow)
-    mla::mla_compact_kernel<64, 256, 4><<<grid, 256, 0, stream>>>(p);
+    compact_launch<64, 256, 4, 3, 3>(p, grid, stream);
   else if (planes * p.slices > sms)
-    mla::mla_compact_kernel<32, 512, 4><<<grid, 512, 0, stream>>>(p);
+    compact_launch<32, 512, 2, 4, 2>(p, grid, stream);
   else
-    mla::mla_compact_kernel<32, 1024, 4><<<grid, 1024, 0, stream>>>(p);
+    compact_launch<32, 1024, 2, 5, 1>(p, grid, stream);
   MLA_CUDA(cudaGetLastError());
   return MLA_OK;
 }

@@ -14,11 +14,11 @@
 //
 // What bounds it: HBM, one read and one write of every moved row.  The slices of a request are
 // neighbouring CTAs, which walk the rows at the same pace, so the 128-byte lines they share are
-// fetched once.  A request has 9 slices of 576 bytes, four CTAs of 256 threads to an SM (128 requests of 8k
-// cut to 4k: 119 us, 0.79 of the copy rate; two of 512: 128).  With few requests the slices are 32 bytes wide
-// (a DRAM sector) and the CTAs larger, and what is in flight per SM bounds it (4 requests of 128k cut to
-// 64k: 146 us, 0.32; a cluster per slice, whose barrier waits for the writes, gave 141 and cost the full
-// batches 13 %).
+// fetched once.  A request has 9 slices of 576 bytes; 128 requests of 8k cut to 4k take 120 us, 0.78 of the
+// copy rate.  With few requests the slices are 32 bytes wide (a DRAM sector) and the CTAs larger, and what
+// bounds it is the rate at which an SM's load unit takes scattered 32-byte pieces: 4 requests of 128k cut to
+// 64k 116 us, 0.4 of the copy rate on 72 SMs.  (Copies held in registers instead of shared memory: 119 and
+// 146; a cluster per slice, whose barrier waits for the writes: 134 and 141.)
 #pragma once
 #include <cstdint>
 #include "mla_kernels.cuh"
@@ -117,77 +117,91 @@ __device__ __forceinline__ void compact_walk(const CompactParams& p, const int32
 }
 
 // The cache rows: a CTA moves one slice of SLICE bytes of every row, SLICE / 16 lanes per row, U rows per
-// lane and chunk.  The three dependent rounds of a chunk overlap with the chunks before it: while chunk n
-// waits for its barrier and is written, chunk n + 1's rows are on their way and chunk n + 2's pages are
-// looked up.  (Its rows may be read before chunk n is written: they lie at or above chunk n + 1.)
-template <int SLICE, int THREADS, int U>
+// lane and chunk.  A chunk passes four stations, one per turn of the loop: its kept indices are loaded, its
+// pages looked up, its rows copied into shared memory (cp.async, S chunks deep, each lane into slots of its
+// own), and, once all of the CTA's copies of the chunk are in, written.  Rows may be read before earlier
+// chunks are written: they lie at or above their own chunk.
+constexpr uint32_t CMP_SLOT = 20;                        // bytes per lane, row and chunk: 16 and the row it goes to
+template <int SLICE, int THREADS, int U, int S>
 __device__ __forceinline__ void compact_rows(const CompactParams& p, const int32_t* kept, uint32_t m, const uint32_t* lut,
                                              int plane, int slice) {
   constexpr int LPR = SLICE / 16;                        // lanes per row
-  constexpr uint32_t ROWS = THREADS / LPR;           // rows of a chunk per step u
+  constexpr uint32_t ROWS = THREADS / LPR;               // rows of a chunk per step u
   constexpr uint32_t CHUNK = ROWS * U;
   constexpr uint32_t NONE = ~0u;
+  extern __shared__ __align__(16) uint8_t cmp_smem[];
+  const uint32_t data = ptx::smem_u32(cmp_smem) + threadIdx.x * 16;                                   // [S][U][THREADS]
+  uint32_t* dest = reinterpret_cast<uint32_t*>(cmp_smem + S * U * THREADS * 16) + threadIdx.x;        // [S][U][THREADS]
   uint8_t* base = p.blocks + slice * SLICE + (threadIdx.x & (LPR - 1)) * 16;
   const uint32_t j0 = threadIdx.x / LPR;
   const uint32_t kv = static_cast<uint32_t>(plane) * p.NL + p.layer, pages = static_cast<uint32_t>(p.KVD) * p.NL;
-  // rows of a chunk: kept index and own index of each step; then pool rows (NONE: nothing to move)
-  auto indices = [&](uint32_t c0, uint32_t (&from)[U]) {
+  const uint32_t chunks = (m + CHUNK - 1) / CHUNK;
+  uint32_t from[U];                                      // station 1: sources of chunk c
+  auto indices = [&](uint32_t c) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t j = c0 + u * ROWS + j0;
+      const uint32_t j = c * CHUNK + u * ROWS + j0;
       from[u] = j < m ? static_cast<uint32_t>(kept[j]) : j;
     }
   };
-  auto rows = [&](uint32_t c0, const uint32_t (&from)[U], uint32_t (&src)[U], uint32_t (&dst)[U]) {
+  uint32_t fb[U], tb[U], fs[U], ts[U];                   // station 2: blocks (NONE: no such page) and slots
+  auto lookup = [&](uint32_t c) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t j = c0 + u * ROWS + j0, f = from[u];
-      src[u] = NONE;
-      dst[u] = NONE;
-      if (f == j) continue;                              // already in its place
+      const uint32_t j = c * CHUNK + u * ROWS + j0, f = from[u];
       const uint32_t fp = p.divP.div(f), tp = p.divP.div(j);
+      fs[u] = f - fp * p.P;
+      ts[u] = f == j ? NONE : j - tp * p.P;              // NONE: already in its place
       const bool in = f > j && fp < static_cast<uint32_t>(p.max_pages);
-      const uint32_t fb = in ? lut[fp] : NONE, tb = in ? lut[tp] : NONE;
-      if (fb < static_cast<uint32_t>(p.NB) && tb < static_cast<uint32_t>(p.NB)) {
-        src[u] = (fb * pages + kv) * p.P + (f - fp * p.P);   // below 2^31: the pool's rows are
-        dst[u] = (tb * pages + kv) * p.P + (j - tp * p.P);
-      } else {
-        raise_status(p.status, STATUS_BOUNDS);           // left as it is
-      }
+      fb[u] = in ? lut[fp] : NONE;
+      tb[u] = in ? lut[tp] : NONE;
     }
   };
-  uint32_t from[U], src[U], dst[U], next_dst[U];
-  uint4 v[U], next[U];
-  auto load = [&](uint4 (&to)[U]) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (src[u] != NONE) to[u] = ld_row(reinterpret_cast<const uint4*>(base + static_cast<size_t>(src[u]) * p.row_bytes));
-  };
-  indices(0, from);
-  rows(0, from, src, dst);
-  load(v);
-  indices(CHUNK, from);
-  rows(CHUNK, from, src, next_dst);
-  indices(2 * CHUNK, from);
-  for (uint32_t c0 = 0; c0 < m; c0 += CHUNK) {
-    load(next);                                          // chunk n + 1
-    __syncthreads();                                     // chunk n has been read by every thread
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (dst[u] != NONE) *reinterpret_cast<uint4*>(base + static_cast<size_t>(dst[u]) * p.row_bytes) = v[u];
+  auto copy = [&](uint32_t s) {                          // station 3, into slots s
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      v[u] = next[u];
-      dst[u] = next_dst[u];
+      uint32_t d = NONE;
+      if (ts[u] != NONE) {
+        if (fb[u] < static_cast<uint32_t>(p.NB) && tb[u] < static_cast<uint32_t>(p.NB)) {
+          const uint32_t src = (fb[u] * pages + kv) * p.P + fs[u];   // below 2^31: the pool's rows are
+          d = (tb[u] * pages + kv) * p.P + ts[u];
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                       :: "r"(data + (s * U + u) * THREADS * 16), "l"(base + static_cast<size_t>(src) * p.row_bytes) : "memory");
+        } else {
+          raise_status(p.status, STATUS_BOUNDS);         // left as it is
+        }
+      }
+      dest[(s * U + u) * THREADS] = d;
     }
-    rows(c0 + 2 * CHUNK, from, src, next_dst);
-    indices(c0 + 3 * CHUNK, from);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  indices(0);
+  for (uint32_t c = 0; c < S; ++c) {                     // chunks 0 .. S - 2 on their way, S - 1 looked up
+    lookup(c);
+    indices(c + 1);
+    if (c < S - 1) copy(c);
   }
+  uint32_t s = 0;
+  for (uint32_t c = 0; c < chunks; ++c) {
+    copy(s == 0 ? S - 1 : s - 1);                        // chunk c + S - 1, where chunk c - 1 was
+    lookup(c + S);
+    indices(c + S + 1);
+    asm volatile("cp.async.wait_group %0;" :: "n"(S - 1) : "memory");
+    __syncthreads();                                     // chunk c has been read by every thread
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t d = dest[(s * U + u) * THREADS];
+      if (d != NONE)
+        *reinterpret_cast<uint4*>(base + static_cast<size_t>(d) * p.row_bytes) = ptx::ld_shared_v4(data + (s * U + u) * THREADS * 16);
+    }
+    s = s + 1 == S ? 0 : s + 1;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // grid (kv planes * slices + kv planes (scales) + 1 (accumulated weights), requests)
-template <int SLICE, int THREADS, int U>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) mla_compact_kernel(const __grid_constant__ CompactParams p) {
+template <int SLICE, int THREADS, int U, int S, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) mla_compact_kernel(const __grid_constant__ CompactParams p) {
   const int b = blockIdx.y;
   const int32_t given = p.kept_lengths[b];
   const uint32_t m = min(max(given, 0), p.max_kept);
@@ -199,7 +213,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) mla_compact_kernel(co
   int i = blockIdx.x;
   if (i < p.KVD * p.slices) {
     const int plane = i / p.slices, slice = i - plane * p.slices;
-    compact_rows<SLICE, THREADS, U>(p, kept, m, lut, plane, slice);
+    compact_rows<SLICE, THREADS, U, S>(p, kept, m, lut, plane, slice);
     return;
   }
   i -= p.KVD * p.slices;
