@@ -29,8 +29,8 @@ cudaError_t mha_smem() {
 }
 
 // The current device's SM count and status word, and (once per device) the shared-memory limits of the kernels here.
-mla_status_t cache_device(int* sms, unsigned int** status) {
-  static int g_sms[kMaxDevices];
+mla_status_t cache_device(int* sms, unsigned int** status, int* wide_clusters = nullptr) {
+  static int g_sms[kMaxDevices], g_wide[kMaxDevices];
   static unsigned int* g_status[kMaxDevices];
   int dev = 0;
   MLA_CUDA(cudaGetDevice(&dev));
@@ -54,8 +54,26 @@ mla_status_t cache_device(int* sms, unsigned int** status) {
     MLA_CUDA((mha_smem<128, true>()));
     g_status[dev] = status_ptr();
     if (!g_status[dev]) return fail(MLA_ERR_CUDA, "status word address unavailable");
+    // clusters of 16 (more than the portable size) of the selection that the device holds at once
+    MLA_CUDA(cudaFuncSetAttribute(mla::mla_select_kernel<1024>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16 * 64);
+    cfg.blockDim = dim3(1024);
+    cfg.dynamicSmemBytes = mla::SEL_KEYS_OFF + mla::SEL_CACHE * 4;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&g_wide[dev], mla::mla_select_kernel<1024>, &cfg) != cudaSuccess) {
+      g_wide[dev] = 0;
+      cudaGetLastError();
+    }
     g_sms[dev] = n;
   }
+  if (wide_clusters) *wide_clusters = g_wide[dev];
   *status = g_status[dev];
   *sms = g_sms[dev];
   return MLA_OK;
@@ -402,9 +420,9 @@ mla_status_t mla_select_keys(const float* scores, int64_t scores_stride, const u
   const int64_t most = budget < static_cast<int64_t>(max_length) ? budget : static_cast<int64_t>(max_length);
   if (kept_stride < most) return fail(MLA_ERR_INVALID_ARG, "the rows of kept must hold %lld values", static_cast<long long>(most));
   if (batch == 0) return MLA_OK;
-  int sms = 0;
+  int sms = 0, wide_clusters = 0;
   unsigned int* status = nullptr;
-  mla_status_t st = cache_device(&sms, &status);
+  mla_status_t st = cache_device(&sms, &status, &wide_clusters);
   if (st != MLA_OK) return st;
   mla::SelectParams p{};
   p.scores = scores;
@@ -419,16 +437,22 @@ mla_status_t mla_select_keys(const float* scores, int64_t scores_stride, const u
   p.recent = num_recent;
   p.sink = num_sink;
   // CTAs per request: about 2048 keys each, up to the portable cluster size, while all of them fit on the
-  // device at once (128 requests of 8k: 18 us with 2, 30 with 4 in two waves); of 512 threads, and of 1024
-  // where a CTA has more than 8192 keys (4 of 128k: 25 us, 30 with 512; 32 of 4k: 15.4, 13.4 with 512).
+  // device at once (two of 512 threads to an SM, or one of 1024, which a CTA with more than 4096 keys gets):
+  // 128 requests of 8k take 19 us with 2, 30 with 4 in two waves; 4 of 128k 26 us, 31 with 512 threads; 32
+  // of 4k 13.5, 15.4 with 1024.  A few long requests take clusters of 16, where the device has room for all.
+  auto fits = [&](int n) {
+    return static_cast<int64_t>(batch) * n <= (max_length > static_cast<uint32_t>(n) * 4096 ? sms : 2 * sms);
+  };
   int ncta = 1;
-  while (ncta < 8 && static_cast<uint32_t>(ncta) * 2048 < max_length && static_cast<int64_t>(batch) * ncta * 2 <= 2 * sms) ncta *= 2;
+  while (ncta < 8 && static_cast<uint32_t>(ncta) * 2048 < max_length && fits(2 * ncta)) ncta *= 2;
+  if (ncta == 8 && max_length > 65536 && batch <= wide_clusters) ncta = 16;
   if (static_cast<int64_t>(batch) * ncta > 0x7FFFFFFF) return fail(MLA_ERR_UNSUPPORTED, "batch too large");
   const uint32_t per = (max_length + ncta - 1) / ncta;
   const uint32_t cached = per < static_cast<uint32_t>(mla::SEL_CACHE) ? per : mla::SEL_CACHE;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(batch) * ncta);
-  cfg.blockDim = dim3(per > 8192 ? 1024 : 512);
+  const bool large = per > 4096;
+  cfg.blockDim = dim3(large ? 1024 : 512);
   cfg.dynamicSmemBytes = mla::SEL_KEYS_OFF + cached * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -438,7 +462,7 @@ mla_status_t mla_select_keys(const float* scores, int64_t scores_stride, const u
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (per > 8192)
+  if (large)
     MLA_CUDA(cudaLaunchKernelEx(&cfg, mla::mla_select_kernel<1024>, p));
   else
     MLA_CUDA(cudaLaunchKernelEx(&cfg, mla::mla_select_kernel<512>, p));

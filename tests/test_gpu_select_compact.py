@@ -58,6 +58,19 @@ def test_select_more_keys_than_a_cluster_holds():
     assert torch.equal(got[0].cpu().long(), want)
 
 
+@pytest.mark.parametrize("B,n", [(1, 700_001), (9, 330_000), (7, 66_000), (8, 66_000)])
+def test_select_long_requests(B, n):
+    """Clusters of 8 and 16, with all keys held and with some read again."""
+    x = weights(B, n, 5, "ties")
+    lengths = torch.tensor([n - 17 * b for b in range(B)], dtype=torch.int32)
+    got, count = M.select_keys(x.cuda(), lengths.cuda(), n, n // 3, 9, 2)
+    assert M.device_status() == 0 and (count == n // 3).all()
+    for b, m in enumerate(lengths.tolist()):
+        order = torch.sort(x[b, 2:m - 9], descending=True, stable=True).indices[:n // 3 - 11] + 2
+        want = torch.cat([torch.arange(2), order.sort().values, torch.arange(m - 9, m)])
+        assert torch.equal(got[b].cpu().long(), want)
+
+
 def test_select_strided_rows_many_requests_and_a_long_length():
     B = 300
     x = weights(B, 200, 5, "ties")
