@@ -369,27 +369,27 @@ def _rows(name, t, dtype, batch, cols):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must have dtype {dtype} (got {t.dtype})")
-    if t.dim() != 2 or t.shape[0] != batch or t.shape[1] < cols:
-        raise ValueError(f"{name} must be [{batch}, >= {cols}] (got shape {tuple(t.shape)})")
-    n = t.shape[1]
-    if batch <= 1:
-        if n > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name} must have contiguous rows")
-        return n
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != batch or shape[1] < cols:
+        raise ValueError(f"{name} must be [{batch}, >= {cols}] (got shape {tuple(shape)})")
+    n = shape[1]
     step, inner = t.stride()
-    if (n > 1 and inner != 1) or step < n:
+    if inner != 1 and n > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if batch <= 1:
+        return n
+    if step < n:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
     return step
 
 
-def _apart(name, t, tstep, other, u, ustep, cols):
-    """Refuses two row buffers that overlap in part (columns of one wide buffer may interleave)."""
-    a, b, size = t.data_ptr(), u.data_ptr(), 4 * cols
-    if a + 4 * ((t.shape[0] - 1) * tstep + cols) <= b or b + 4 * ((u.shape[0] - 1) * ustep + cols) <= a:
+def _apart(name, t, tstep, other, u, ustep, batch, cols):
+    """Refuses two fp32 row buffers that overlap in part (columns of one wide buffer may interleave)."""
+    a, b = t.data_ptr(), u.data_ptr()
+    if a + 4 * ((batch - 1) * tstep + cols) <= b or b + 4 * ((batch - 1) * ustep + cols) <= a:
         return
-    if tstep == ustep and size <= (b - a) % (4 * tstep) <= 4 * tstep - size:
-        return
-    raise ValueError(f"{name} must be {other} itself or not overlap it")
+    if (a != b or tstep != ustep) and not (tstep == ustep and 4 * cols <= (b - a) % (4 * tstep) <= 4 * (tstep - cols)):
+        raise ValueError(f"{name} must be {other} itself or not overlap it")
 
 
 def _one_device(first, *rest):
@@ -413,7 +413,7 @@ def _raw_stream(stream, device):
 
 def _run(device, fn, *args):
     """One library call, on the tensors' device whatever the current one."""
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         st = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -459,6 +459,19 @@ def _check_scale_table(lookup_table, scales_lookup_table):
             raise ValueError("scales_lookup_table must have the shape of lookup_table")
 
 
+def _cache_shape(blocks, scales, scales_lookup_table, batch, heads, v_dim, lookup_table):
+    """Shape record of a cache whose scales, where it has them, hold each token's in the last dim."""
+    NB, KVD, NL, P, NKV, D = blocks.shape
+    NSB, g = NB, 1
+    if scales is not None:
+        NSB, sKVD, sNL, sP, sNKV, g = scales.shape
+        if sKVD != KVD or sNL != NL or sP != P or sNKV != NKV:
+            raise ValueError("scales must match blocks in kv_dim, num_layers, page_size and num_heads")
+        if NSB != NB and scales_lookup_table is None:
+            raise ValueError("without a scales_lookup_table, scales must have as many blocks as blocks")
+    return PagedShape(batch, heads, D, v_dim, NB, KVD, NL, P, NKV, NSB, g, lookup_table.shape[1])
+
+
 def _token_count(max_prompt_length, tokens):
     if max_prompt_length != tokens:
         raise ValueError(f"max_prompt_length must be q's number of tokens, {tokens} (got {max_prompt_length})")
@@ -486,15 +499,12 @@ def accumulate_weights(q, lse, blocks, scales, cache_lengths, lookup_table, scal
         _expect("scales", scales, (_F32,), ndim=6)
     _check_tables(cache_lengths, lookup_table, scales_lookup_table, B)
     _token_count(max_prompt_length, T)
-    shp = paged_shape(B, H, blocks, scales, lookup_table)
-    if scales.shape[1:5] != (shp.kv_dim, shp.num_layers, shp.page_size, shp.num_kv_heads):
-        raise ValueError("scales must match blocks in kv_dim, num_layers, page_size and num_heads")
-    if scales_lookup_table is None and shp.num_scale_blocks != shp.num_blocks:
-        raise ValueError("without a scales_lookup_table, scales must have as many blocks as blocks")
+    shp = _cache_shape(blocks, scales, scales_lookup_table, B, H, 512, lookup_table)
     need = max_cache_length + T
     sstep = 0 if scores is None else _rows("scores", scores, _F32, B, need)
     ostep = 0 if out is None else _rows("out", out, _F32, B, need)
-    _expect("workspace", workspace, (_U8,), ndim=1, optional=True)
+    if workspace is not None:
+        _expect("workspace", workspace, (_U8,), ndim=1)
     dev = _one_device(q, lse, blocks, scales, cache_lengths, lookup_table, scales_lookup_table, scores, out, workspace)
     lib = load()
     if out is None:
@@ -504,8 +514,8 @@ def accumulate_weights(q, lse, blocks, scales, cache_lengths, lookup_table, scal
             ostep = need
         else:
             out, ostep = scores, sstep
-    elif scores is not None and (out.data_ptr() != scores.data_ptr() or ostep != sstep):
-        _apart("out", out, ostep, "scores", scores, sstep, need)
+    elif scores is not None and out is not scores:
+        _apart("out", out, ostep, "scores", scores, sstep, B, need)
     if B == 0:
         return out
     if workspace is None:
@@ -566,7 +576,8 @@ def compact_cache(kept, kept_lengths, lookup_table, scales_lookup_table, layer_i
     Returns (blocks, scales, scores)."""
     if not _plain(blocks, _U8, 6):
         _expect("blocks", blocks, _CODES + (_BF16,), ndim=6)
-    _expect("scales", scales, (_F32,), ndim=6, optional=True)
+    if not _plain(scales, _F32, 6):
+        _expect("scales", scales, (_F32,), ndim=6, optional=True)
     if not (_plain(kept_lengths, _I32, 1) and _plain(lookup_table, _I32, 2)):
         _expect("kept_lengths", kept_lengths, (_I32,), ndim=1)
         _expect("lookup_table", lookup_table, _U32, ndim=2)
@@ -575,19 +586,11 @@ def compact_cache(kept, kept_lengths, lookup_table, scales_lookup_table, layer_i
         raise ValueError(f"lookup_table must have {B} rows (one per request)")
     _check_scale_table(lookup_table, scales_lookup_table)
     kstep = _rows("kept", kept, _I32, B, 1)
-    NB, KVD, NL, P, NKV, D = blocks.shape
-    NSB, g = NB, 1
-    if scales is not None:
-        NSB, g = scales.shape[0], scales.shape[5]
-        if scales.shape[1:5] != (KVD, NL, P, NKV):
-            raise ValueError("scales must match blocks in kv_dim, num_layers, page_size and num_heads")
-        if scales_lookup_table is None and NSB != NB:
-            raise ValueError("without a scales_lookup_table, scales must have as many blocks as blocks")
+    shp = _cache_shape(blocks, scales, scales_lookup_table, B, 0, 0, lookup_table)
     sstep = 0 if scores is None else _rows("scores", scores, _F32, B, 1)
     dev = _one_device(kept, kept_lengths, lookup_table, scales_lookup_table, blocks, scales, scores)
     if B == 0:
         return blocks, scales, scores
-    shp = PagedShape(B, 0, D, 0, NB, KVD, NL, P, NKV, NSB, g, lookup_table.shape[1])
     _run(dev, load().mla_compact_paged, kept.data_ptr(), kstep, kept.shape[1], kept_lengths.data_ptr(),
          lookup_table.data_ptr(), _adr(scales_lookup_table), int(layer_idx), blocks.element_size(), ctypes.byref(shp),
          blocks.data_ptr(), _adr(scales), _adr(scores), sstep, 0 if scores is None else scores.shape[1],
@@ -658,7 +661,8 @@ def mha_decode(q, blocks, scales, cache_lengths, lookup_table, scales_lookup_tab
         raise ValueError(f"out must be a contiguous bf16 tensor of shape {tuple(q.shape)}")
     if lse is not None and (not _plain(lse, _F32, 3) or lse.shape != (B, T, H)):
         raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(B, T, H)}")
-    _expect("workspace", workspace, (_U8,), ndim=1, optional=True)
+    if workspace is not None:
+        _expect("workspace", workspace, (_U8,), ndim=1)
     dev = _one_device(q, blocks, scales, cache_lengths, lookup_table, scales_lookup_table, out, lse, workspace)
     lib = load()
     if out is None or (lse is None and want_lse):

@@ -81,12 +81,13 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) mla_select_kernel(const __grid
   const uint32_t n = min(given, p.max_length);
   const uint32_t count = min(n, static_cast<uint32_t>(p.budget));
   int32_t* out = p.kept + b * p.kept_stride;
-  // kept_lengths may be lengths: it is written once every CTA of the cluster has read the length
-  ptx::cluster_sync();
-  if (rank == 0 && tid == 0) {
-    if (given > p.max_length) raise_status(p.status, STATUS_BOUNDS);
-    p.kept_lengths[b] = static_cast<int32_t>(count);
-  }
+  // kept_lengths may be lengths: it is written behind a barrier that every CTA reaches with the length read
+  auto write_count = [&]() {
+    if (rank == 0 && tid == 0) {
+      if (given > p.max_length) raise_status(p.status, STATUS_BOUNDS);
+      p.kept_lengths[b] = static_cast<int32_t>(count);
+    }
+  };
   // the protected ends (and, within the budget, every key)
   const bool all = n <= static_cast<uint32_t>(p.budget);
   const uint32_t head = all ? n : p.sink, tail = all ? 0 : p.recent;
@@ -94,7 +95,11 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) mla_select_kernel(const __grid
   for (uint32_t j = gtid; j < head; j += gthreads) out[j] = static_cast<int32_t>(j);
   for (uint32_t j = gtid; j < tail; j += gthreads) out[count - tail + j] = static_cast<int32_t>(n - tail + j);
   const uint32_t need0 = count - head - tail;            // keys to choose from the middle
-  if (need0 == 0) return;                                // the same for every CTA of the cluster
+  if (need0 == 0) {                                      // the same for every CTA of the cluster
+    ptx::cluster_sync();
+    write_count();
+    return;
+  }
 
   // this CTA's share [lo, hi) of the middle, and each warp's share of that (multiples of 32 keys, so
   // that indices ascend over lanes, steps, warps and CTAs)
@@ -156,6 +161,7 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) mla_select_kernel(const __grid
         s.hist[0][i] = s.hist0[i][0] + s.hist0[i][1] + s.hist0[i][2] + s.hist0[i][3];
     }
     ptx::cluster_sync();                                 // every CTA's histogram is complete
+    if (d == 0) write_count();
     const uint32_t slice = bins[d] / ncta;
     for (uint32_t i = tid; i < slice; i += SEL_THREADS) {
       const uint32_t bin = rank * slice + i;
