@@ -350,9 +350,10 @@ mla_status_t mla_merge_lse_parts_bf16(const void* outs, const float* lses, int32
  *                 the split q.  It is the caller's: calls that overlap on the device, or captured graphs
  *                 that are replayed at the same time, need one each.  Nothing in it has to start at zero
  *                 and nothing is kept in it from call to call.
- * Rows hold at least max_cache_length + max_prompt_length values (else MLA_ERR_INVALID_ARG).  The
- * first call on a device is made outside stream capture.  The keys of a page id past the pool are left as they were and flagged
- * (MLA_ERR_DEVICE_BOUNDS), and a length above max_cache_length is clamped to it and flagged.
+ * Rows hold at least max_cache_length + max_prompt_length values (else MLA_ERR_INVALID_ARG).  The keys of
+ * a page id past the pool are left as they were and flagged (MLA_ERR_DEVICE_BOUNDS), and a length above
+ * max_cache_length is clamped to it and flagged.  (As for the entry points below, the first call on a
+ * device is made outside stream capture.)
  */
 mla_status_t mla_accumulate_weights_fp8(
     const void* q, const float* lse, const void* blocks, const float* scales,
@@ -377,7 +378,7 @@ mla_status_t mla_accumulate_workspace_bytes(uint32_t max_prompt_length, const ml
  *                 clamped to it and flagged, MLA_ERR_DEVICE_BOUNDS)
  *   budget        >= 1; num_recent, num_sink >= 0 with num_recent + num_sink <= budget
  *   kept          int32, row b at kept + b * kept_stride (kept_stride >= min(budget, max_length))
- *   kept_lengths  int32 [batch], written; may be lengths itself
+ *   kept_lengths  int32 [batch], written; may be lengths itself, else must not overlap it (MLA_ERR_INVALID_ARG)
  * No workspace; batch = 0 is a no-op.
  */
 mla_status_t mla_select_keys(
@@ -435,7 +436,9 @@ mla_status_t mla_mha_kv_store(
  *     x[t] = softmax_scale <q[b,i,h,:], K[t]> for t <= cache_lengths[b] + i,
  *     lse  = ln sum_t exp(x[t]),  out[b,i,h,:] = sum_t exp(x[t] - lse) V[t],
  * with K and V the stored bf16 values, or e4m3 * scale unrounded.  Keys, values and scales of the
- * stored tokens are to be finite; what the cache holds behind a request's end is never used.
+ * stored tokens are to be finite; what the cache holds behind a request's end is never used.  Weights are
+ * rounded to bf16, or for e4m3 to 11 bits with V's scale folded in: all 11 while V's scale is above 2^-23 of
+ * the largest of the request and head (rows of zeros included, whose scale mla_mha_kv_store sets to 1).
  *
  *   q          bf16 [batch, max_prompt_length, num_q_heads, head_dim], 16-byte aligned
  *   out        bf16, as q, not overlapping it; lse fp32 [batch, max_prompt_length, num_q_heads], natural log, or NULL

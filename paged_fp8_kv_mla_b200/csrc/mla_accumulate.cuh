@@ -79,7 +79,7 @@ constexpr uint32_t ACC_WIDE_BYTES = ACC_BN * 128, ACC_NARROW_BYTES = ACC_BN * 64
 constexpr uint32_t ACC_SH = 0;                    // [2][128] {factor, -lse log2 e}
 constexpr uint32_t ACC_SBAR = ACC_SH + 2 * ACC_HEADS * 8;
 constexpr uint32_t ACC_SMISC = ACC_SBAR + 512;
-constexpr uint32_t ACC_SQ = 3072;
+constexpr uint32_t ACC_SQ = 3 * 1024;
 constexpr uint32_t ACC_SMEM_ALLOC = 232448;
 static_assert(ACC_SMISC + 256 <= ACC_SQ && ACC_SQ % 1024 == 0, "scalars overlap q");
 __host__ __device__ constexpr uint32_t acc_wide_slots(uint32_t hpad) {

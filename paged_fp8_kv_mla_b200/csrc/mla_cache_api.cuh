@@ -79,6 +79,10 @@ mla_status_t cache_device(int* sms, unsigned int** status, int* wide_clusters = 
   return MLA_OK;
 }
 
+bool overlap(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // A paged array's pool and page-table description, for any row width; the latent cache's own checks
@@ -206,6 +210,7 @@ mla_status_t mha_plan(const mla_paged_shape_t* s, uint32_t T, uint32_t max_cache
   m.tile = 16 * m.ks * m.kw;
   while (m.tile < 128 && 2 * m.tile * per_key <= 73728) m.tile *= 2;
   m.box_rows = gcd_int(s->page_size, m.tile);
+  if (m.box_rows > 256) m.box_rows = 256;                // (both are powers of two) a box's largest extent
   m.plane_bytes = static_cast<uint32_t>(m.tile) * m.hg * s->head_dim * element_bytes;
   m.stage_bytes = static_cast<uint32_t>(align_up(m.tile * per_key, 1024));
   const uint32_t merge = m.kw > 1 ? (s->head_dim == 64 ? mla::mha_merge_bytes<64>() : mla::mha_merge_bytes<128>()) : 0;
@@ -420,6 +425,8 @@ mla_status_t mla_select_keys(const float* scores, int64_t scores_stride, const u
   const int64_t most = budget < static_cast<int64_t>(max_length) ? budget : static_cast<int64_t>(max_length);
   if (kept_stride < most) return fail(MLA_ERR_INVALID_ARG, "the rows of kept must hold %lld values", static_cast<long long>(most));
   if (batch == 0) return MLA_OK;
+  if (static_cast<const void*>(kept_lengths) != lengths && overlap(kept_lengths, 4ull * batch, lengths, 4ull * batch))
+    return fail(MLA_ERR_INVALID_ARG, "kept_lengths must be lengths itself or not overlap it");
   int sms = 0, wide_clusters = 0;
   unsigned int* status = nullptr;
   mla_status_t st = cache_device(&sms, &status, &wide_clusters);
@@ -614,7 +621,8 @@ mla_status_t mla_mha_decode_paged(const void* q, const void* blocks, const float
   if (!(softmax_scale == softmax_scale)) return fail(MLA_ERR_INVALID_ARG, "softmax_scale is NaN");
   MhaPlan m{};
   if (s->batch == 0) return mha_plan(s, max_prompt_length, max_cache_length, element_bytes, 1, &m);
-  if (q == out) return fail(MLA_ERR_INVALID_ARG, "out must not be q");
+  const uint64_t q_bytes = 2ull * s->batch * max_prompt_length * s->num_q_heads * s->head_dim;
+  if (overlap(q, q_bytes, out, q_bytes)) return fail(MLA_ERR_INVALID_ARG, "out must not be q, nor overlap it");
   int sms = 0;
   unsigned int* status = nullptr;
   st = cache_device(&sms, &status);

@@ -22,7 +22,7 @@
 // e4m3.  The values are converted to f16, exactly, as they leave shared memory (two per instruction),
 // and never to anything wider: q is brought to f16 with a power of two (exact down to 2^-30 of the
 // largest value), K's scale multiplies the score, and V's scale goes into the weight, relative to a
-// running power-of-two bound of V's scales so that f16 holds it with 11 bits.  The instructions of this
+// running power-of-two bound of V's scales so that f16 holds it with 11 bits (down to 2^-23 of the bound).  The instructions of this
 // are what keeps an e4m3 cache from the copy rate: the loads alone run at it.
 //
 // Work split.  The tiles of all (request, head group, row group) items, with each item's fixed cost, laid
@@ -293,6 +293,10 @@ struct MhaRows {
   // running one by at most LAZY (log2): weights stay below 2^LAZY and O is rescaled rarely.  ks, vs: the
   // scales of the step's first key, sstep bytes from key to key; key0: the first key, n: stored keys.
   static constexpr float LAZY = 6.f;
+  // e4m3: a weight times its V scale is stored in f16 as a multiple of vref 2^-VSHIFT, so that at most 2^(LAZY +
+  // VSHIFT), half of f16's range, is stored, and it has all 11 bits while the product is above 2^-23 vref: an
+  // all-zero row, whose scale is 1, costs rows of small values nothing.
+  static constexpr int VSHIFT = 9;
   template <int KS>
   __device__ __forceinline__ void weights(const MhaParams& p, float2 (&s)[KS][NR][2], uint32_t ks, uint32_t vs, uint32_t sstep,
                                           uint32_t key0, uint32_t n, int lane, uint32_t (&pb)[KS][NR][2]) {
@@ -350,7 +354,7 @@ struct MhaRows {
       float ref = vref;
       if (FP8) {
         top = warp_max(top);
-        if (top > vref) ref = pow2(min(max(static_cast<int>(__float_as_uint(top) >> 23) - 126, -126), 126));
+        if (top > vref) ref = pow2(min(max(static_cast<int>(__float_as_uint(top) >> 23) - 126, VSHIFT - 126), 126));
       }
       const float vc = FP8 && ref != vref ? vref / ref : 1.f;
       vref = ref;
@@ -371,8 +375,8 @@ struct MhaRows {
         m[u][1] = m1;
       }
     }
-    // 1 / vref: a power of two's reciprocal has the mirrored exponent
-    const float inv = FP8 && vref > 0.f ? __uint_as_float(0x7F000000u - __float_as_uint(vref)) : 0.f;
+    // 2^VSHIFT / vref: a power of two's reciprocal has the mirrored exponent
+    const float inv = FP8 && vref > 0.f ? __uint_as_float(0x7F000000u + (VSHIFT << 23) - __float_as_uint(vref)) : 0.f;
 #pragma unroll
     for (int u = 0; u < NR; ++u) {
       const float2 r = make_float2(m[u][0] == -INFINITY ? 0.f : -m[u][0], m[u][1] == -INFINITY ? 0.f : -m[u][1]);
@@ -441,6 +445,7 @@ struct MhaRows {
 
   // The whole sums of the rows, and O in its own units.
   __device__ __forceinline__ void finish_sums() {
+    const float unit = vref * pow2(-VSHIFT);
 #pragma unroll
     for (int u = 0; u < NR; ++u) {
       l[u] = make_float2(keys_sum(l[u].x), keys_sum(l[u].y));
@@ -448,7 +453,7 @@ struct MhaRows {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) o[k][u][x] = __fmul2_rn(o[k][u][x], make_float2(vref, vref));
+          for (int x = 0; x < 2; ++x) o[k][u][x] = __fmul2_rn(o[k][u][x], make_float2(unit, unit));
     }
   }
   // Hands the state to, or takes it from, a warp with other keys of the same rows.

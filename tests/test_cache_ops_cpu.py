@@ -230,3 +230,18 @@ def test_workspace_size_of_the_binding():
     assert M.accumulate_workspace_bytes(2, 1, 16) == 2 * 16 * (2 * 576 + 8)
     with pytest.raises(M.MlaError):
         M.accumulate_workspace_bytes(2, 0, 16)
+
+
+def test_abi_refuses_partial_overlap(lib):
+    """kept_lengths may be lengths, not a shifted view of it; out must not touch q anywhere."""
+    def select(kl):
+        return lib.mla_select_keys(FAKE, 100, FAKE, 4, 100, 10, 2, 1, FAKE, 10, kl, None)
+    for off in (-12, -4, 4, 12):
+        assert select(FAKE + off) == 1 and "kept_lengths" in lib.mla_last_error_string().decode()
+    nbytes = 2 * 2 * 1 * 16 * 64                                   # of q: batch 2, 16 heads of 64
+
+    def attend(out):
+        return lib.mla_mha_decode_paged(FAKE, FAKE, None, FAKE, FAKE, None, 1, 64, 0, 0.1, 2,
+                                        shape(head_dim=64, v_dim=64, kv_dim=2, num_kv_heads=4), out, None, FAKE, 0, None)
+    for off in (16 - nbytes, -16, 0, 16, nbytes - 16):
+        assert attend(FAKE + off) == 1 and "overlap" in lib.mla_last_error_string().decode()

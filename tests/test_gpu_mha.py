@@ -235,3 +235,45 @@ def test_store_bad_page_is_skipped_and_flagged():
     assert torch.equal(db.cpu(), cache.blocks)
     M.mha_kv_store(k[:, :0], k[:, :0], torch.tensor([16, 16], dtype=torch.int32).cuda(), table, None, 0, db, ds)
     assert M.device_status() == 0
+
+
+@pytest.mark.parametrize("page", [256, 512, 1024])
+@pytest.mark.parametrize("HKV,D,fp8", [(1, 64, True), (1, 64, False), (2, 128, True)])
+def test_decode_large_pages(page, HKV, D, fp8):
+    """Pages of more rows than a copy's box, tiles of more keys than either."""
+    lengths = [1500, 255, 700]
+    cache, q = make(lengths, 1, 8 * HKV, HKV, D, page, fp8, seed=page)
+    out, lse = run(cache, q, lengths, 0.1)
+    check(cache, q, lengths, 0.1, out, lse)
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_zero_value_rows_among_small_ones(D, first):
+    """An all-zero row of V has scale 1, a million times that of its neighbours here; what it may cost them is
+    f16's absolute step at 2^9 times the weight: 2^-34 of V's scale bound (2) per key, times the code, over the
+    sum of the weights, which is at least exp(lse - largest score)."""
+    lengths, HKV, H = [40, 900], 2, 8
+    cache, q = make(lengths, 1, H, HKV, D, 64, True, seed=77)
+    gen = torch.Generator().manual_seed(78)
+    codes = []
+    for b, L in enumerate(lengths):
+        n = L + 1
+        blk, slot = rows_of(cache.table, b, n, 64)
+        x = torch.randn((n, HKV, D), generator=gen) * 2e-4
+        x[0 if first else n - 2] = 0
+        c, s = quantise(x.bfloat16())
+        cache.blocks[blk, 1, 0, slot] = c
+        cache.scales[blk, 1, 0, slot] = s
+        codes.append((cache.rows(1, b, n) / s.double()).abs().sum(0))          # [HKV, D]
+    out, lse = run(cache, q, lengths, D ** -0.5)
+    for b, L in enumerate(lengths):
+        ro, rl, mag, amp = mha_reference(cache, b, q[b], L, D ** -0.5)
+        k = cache.rows(0, b, L + 1)
+        x = torch.einsum("grd,kgd->grk", q[b, 0].double().reshape(HKV, H // HKV, D), k) * D ** -0.5
+        total = torch.exp(rl[0] - x.amax(-1).reshape(H))
+        step = codes[b].repeat_interleave(H // HKV, 0) * 2.0 ** -33 / total[:, None]
+        e = (D + 8) * U * amp + 8 * U * (rl.abs() + amp) + 2.0 ** -21
+        tol = mag * (2.0 ** -11 + 2 * e[..., None] + (L + 65) * U) + ro.abs() * 2.0 ** -8 + step
+        bad = ~((out[b].cpu().double() - ro).abs() <= tol)
+        assert not bad.any(), (b, int(bad.sum()), out[b].cpu().double()[bad][:4], ro[bad][:4], tol[bad][:4])
