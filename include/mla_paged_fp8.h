@@ -337,7 +337,7 @@ mla_status_t mla_merge_lse_parts_bf16(const void* outs, const float* lses, int32
  * key element to bf16, a row's sum is off by that rounding, up to a few 1e-3).  q enters exactly: each
  * head's row is split into two e4m3 terms after scaling by a power of two (elements below 2^-13 of the
  * row's largest are off by at most 2^-21 of it).  A (query token, head) whose lse is -inf adds nothing;
- * a non-finite q row or lse makes the request's sums NaN, a NaN code only its own key's.  Sums are fp32
+ * a non-finite q row or a NaN lse makes the request's sums NaN, a NaN code only its own key's.  Sums are fp32
  * in a fixed order: results are the same from run to run.
  *
  *   q, blocks, ... , shape   as for mla_decode_paged_fp8, with head_dim_granularity 1 (else
