@@ -45,7 +45,7 @@ struct SelectShared {
                                    // exponents, which the lanes of a warp share)
   uint32_t hist[3][SEL_BINS];
   uint32_t total[SEL_BINS];
-  uint32_t counts[SEL_MAX_CLUSTER][2];   // kept and tied keys of each CTA of the cluster
+  uint32_t cta_gt[SEL_MAX_CLUSTER], cta_eq[SEL_MAX_CLUSTER];   // kept and tied keys of each CTA of the cluster
   uint32_t warp_gt[SEL_MAX_WARPS], warp_eq[SEL_MAX_WARPS];
   uint32_t scan[SEL_MAX_WARPS];
   uint32_t bin, need;
@@ -60,10 +60,19 @@ __device__ __forceinline__ uint32_t select_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t cluster_addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(cluster_addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};"
+               :: "r"(cluster_addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// Sum of the words before `below` of a warp-sized table (n <= 32 of them used), the same for every lane.
+__device__ __forceinline__ uint32_t sum_below(const uint32_t* table, int n, int below, int lane) {
+  return __reduce_add_sync(0xffffffffu, lane < n && lane < below ? table[lane] : 0u);
 }
 
 template <int SEL_THREADS>
@@ -77,7 +86,8 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) mla_select_kernel(const __grid
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ncta));
   const uint32_t rank = ptx::cluster_ctarank();
   const int b = static_cast<int>(ptx::cluster_id_x());
-  const uint32_t given = p.lengths[b];
+  const uint32_t given = p.lengths[b];                   // (on its way while the histograms are cleared)
+  for (uint32_t i = tid; i < 7 * SEL_BINS / 4; i += SEL_THREADS) reinterpret_cast<uint4*>(&s.hist0[0][0])[i] = make_uint4(0, 0, 0, 0);
   const uint32_t n = min(given, p.max_length);
   const uint32_t count = min(n, static_cast<uint32_t>(p.budget));
   int32_t* out = p.kept + b * p.kept_stride;
@@ -107,7 +117,6 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) mla_select_kernel(const __grid
   const uint32_t per = (mid + ncta - 1) / ncta;
   const uint32_t lo = min(rank * per, mid), hi = min(lo + per, mid), m = hi - lo;
   const float* src = p.scores + b * p.scores_stride + head + lo;
-  for (uint32_t i = tid; i < 7 * SEL_BINS; i += SEL_THREADS) (&s.hist0[0][0])[i] = 0;
   __syncthreads();
 
   // Each pass counts the keys that agree with the digits found so far by their next digit.
@@ -141,6 +150,7 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) mla_select_kernel(const __grid
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        if (i0 + u * SEL_THREADS >= m) break;
         const bool in = i0 + u * SEL_THREADS + tid < m && (d == 0 || (k[u] >> shift[d > 0 ? d - 1 : 0]) == prefix);
         if (!__any_sync(0xffffffffu, in)) continue;
         // one addition per warp where all its keys fall into one bin (equal weights, zeros)
@@ -162,18 +172,38 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) mla_select_kernel(const __grid
     }
     ptx::cluster_sync();                                 // every CTA's histogram is complete
     if (d == 0) write_count();
-    const uint32_t slice = bins[d] / ncta;
-    for (uint32_t i = tid; i < slice; i += SEL_THREADS) {
-      const uint32_t bin = rank * slice + i;
-      uint32_t sum = 0;
-      for (uint32_t q = 0; q < ncta; ++q) sum += ld_cluster_u32(ptx::mapa(ptx::smem_u32(&s.hist[d][bin]), q));
-      for (uint32_t q = 0; q < ncta; ++q) ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&s.total[bin]), q), sum);
-    }
-    ptx::cluster_sync();                                 // every CTA holds the sums
     // the bin of the need-th largest key: thread t owns `each` bins, counted from the top
+    constexpr int MOST = SEL_BINS / SEL_THREADS;
     const int each = bins[d] / SEL_THREADS;              // 4, 2 or 1
+    uint32_t c[MOST] = {};
+    if (ncta == 1) {
+#pragma unroll
+      for (int x = 0; x < MOST; ++x)
+        if (x < each) c[x] = s.hist[d][bins[d] - 1 - (tid * each + x)];
+    } else {
+      // four bins at a time, the CTAs' counts in flight together; each CTA begins with its own
+      const uint32_t slice = bins[d] / ncta;
+      for (uint32_t i = 4 * tid; i < slice; i += 4 * SEL_THREADS) {
+        const uint32_t from = ptx::smem_u32(&s.hist[d][rank * slice + i]), to = ptx::smem_u32(&s.total[rank * slice + i]);
+        uint4 sum = make_uint4(0, 0, 0, 0);
+        for (uint32_t q0 = 0; q0 < ncta; q0 += 4) {
+          uint4 v[4];
+#pragma unroll
+          for (uint32_t u = 0; u < 4; ++u)
+            v[u] = q0 + u < ncta ? ld_cluster_v4(ptx::mapa(from, (rank + q0 + u) & (ncta - 1))) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (uint32_t u = 0; u < 4; ++u) sum = make_uint4(sum.x + v[u].x, sum.y + v[u].y, sum.z + v[u].z, sum.w + v[u].w);
+        }
+        for (uint32_t q = 0; q < ncta; ++q) st_cluster_v4(ptx::mapa(to, (rank + q) & (ncta - 1)), sum);
+      }
+      ptx::cluster_sync();                               // every CTA holds the sums
+#pragma unroll
+      for (int x = 0; x < MOST; ++x)
+        if (x < each) c[x] = s.total[bins[d] - 1 - (tid * each + x)];
+    }
     uint32_t own = 0;
-    for (int x = 0; x < each; ++x) own += s.total[bins[d] - 1 - (tid * each + x)];
+#pragma unroll
+    for (int x = 0; x < MOST; ++x) own += c[x];
     uint32_t inc = own;
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t up = __shfl_up_sync(0xffffffffu, inc, o);
@@ -181,15 +211,14 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) mla_select_kernel(const __grid
     }
     if (lane == 31) s.scan[warp] = inc;
     __syncthreads();
-    uint32_t above = inc - own;
-    for (int w = 0; w < warp; ++w) above += s.scan[w];
-    for (int x = 0; x < each; ++x) {
-      const uint32_t bin = bins[d] - 1 - (tid * each + x), c = s.total[bin];
-      if (above < need && need <= above + c) {
-        s.bin = bin;
+    uint32_t above = inc - own + sum_below(s.scan, SEL_WARPS, warp, lane);
+#pragma unroll
+    for (int x = 0; x < MOST; ++x) {
+      if (x < each && above < need && need <= above + c[x]) {
+        s.bin = bins[d] - 1 - (tid * each + x);
         s.need = need - above;
       }
-      above += c;
+      above += c[x];
     }
     __syncthreads();
     prefix = d == 2 ? (prefix << 10) | s.bin : (prefix << 11) | s.bin;
@@ -212,26 +241,17 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) mla_select_kernel(const __grid
     s.warp_eq[warp] = eq;
   }
   __syncthreads();
-  if (tid < static_cast<int>(ncta)) {
-    uint32_t cg = 0, ce = 0;
-    for (int w = 0; w < SEL_WARPS; ++w) {
-      cg += s.warp_gt[w];
-      ce += s.warp_eq[w];
+  if (warp == 0) {
+    const uint32_t cg = sum_below(s.warp_gt, SEL_WARPS, SEL_WARPS, lane), ce = sum_below(s.warp_eq, SEL_WARPS, SEL_WARPS, lane);
+    if (lane < static_cast<int>(ncta)) {
+      ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&s.cta_gt[rank]), lane), cg);
+      ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&s.cta_eq[rank]), lane), ce);
     }
-    ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&s.counts[rank][0]), tid), cg);
-    ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&s.counts[rank][1]), tid), ce);
   }
   ptx::cluster_sync();                                   // the last access to another CTA's memory
-  uint32_t ties = 0, at = head;                          // ties before this warp, its first output slot
-  for (uint32_t q = 0; q < rank; ++q) {
-    at += s.counts[q][0];
-    ties += s.counts[q][1];
-  }
-  for (int w = 0; w < warp; ++w) {
-    at += s.warp_gt[w];
-    ties += s.warp_eq[w];
-  }
-  at += min(ties, need);
+  // ties before this warp, its first output slot
+  uint32_t ties = sum_below(s.cta_eq, ncta, rank, lane) + sum_below(s.warp_eq, SEL_WARPS, warp, lane);
+  uint32_t at = head + sum_below(s.cta_gt, ncta, rank, lane) + sum_below(s.warp_gt, SEL_WARPS, warp, lane) + min(ties, need);
   const uint32_t below = (1u << lane) - 1;
   for (uint32_t i0 = w0; i0 < w1; i0 += 32) {
     const uint32_t i = i0 + lane;
