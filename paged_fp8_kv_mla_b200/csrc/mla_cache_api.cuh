@@ -445,8 +445,9 @@ mla_status_t mla_select_keys(const float* scores, int64_t scores_stride, const u
   p.sink = num_sink;
   // CTAs per request: about 2048 keys each, up to the portable cluster size, while all of them fit on the
   // device at once (two of 512 threads to an SM, or one of 1024, which a CTA with more than 4096 keys gets):
-  // 128 requests of 8k take 19 us with 2, 30 with 4 in two waves; 4 of 128k 26 us, 31 with 512 threads; 32
-  // of 4k 13.5, 15.4 with 1024.  A few long requests take clusters of 16, where the device has room for all.
+  // 64 requests of 4k take 8.1 us with 2, 9.2 with 1, 11.8 with 4; 128 of 8k 12.5 with 2, 24 with 4 in two
+  // waves; 32 of 40k 15.7, 18.3 with 512 threads; 16 of 16k 12.4, 21 with 1024.  A few long requests take
+  // clusters of 16, where the device has room for all: 4 of 128k 15.6 us, 19.9 with 8.
   auto fits = [&](int n) {
     return static_cast<int64_t>(batch) * n <= (max_length > static_cast<uint32_t>(n) * 4096 ? sms : 2 * sms);
   };

@@ -12,10 +12,12 @@
 // What bounds it.  4 bytes per key are read once; at these sizes (a few MB at most) that is under a
 // microsecond of HBM time, and the time goes to the chain of passes: load, three histograms, output.
 // So a request is spread over a thread-block cluster: every CTA holds its share of the keys in shared
-// memory (read from HBM once), histograms are added up through distributed shared memory (CTA r adds
-// slice r of the bins of all CTAs and hands the sums to all), and the passes are separated by cluster
-// barriers instead of kernel launches.  Measured: 4 requests of 128k keys 20 us, 128
-// of 8k 19 us, 32 of up to 4k 10 us (of which the launch is about 3); half of the issue slots are taken.
+// memory (read from HBM once), histograms are added up through distributed shared memory, and the passes
+// are separated by cluster barriers instead of kernel launches.  Such an access takes some 700 cycles, so
+// they are made in few rounds, all of a round in flight: in clusters of up to 4 every CTA reads all bins of
+// all; in larger ones CTA r adds slice r and hands the sums to all, another barrier later.  Measured (20 or
+// more calls in a graph): 4 requests of 128k keys 15.6 us, 128 of 8k 12.5 us, 32 of up to 4k 8.3 us (of which
+// the launch is about 3); a digit costs 2 us of the last.  (With the bins added one by one: 17.0, 15.6, 11.1.)
 #pragma once
 #include <cstddef>
 #include <cstdint>
@@ -60,15 +62,23 @@ __device__ __forceinline__ uint32_t select_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t cluster_addr) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(cluster_addr) : "memory");
-  return v;
+// c[0 .. n) += n words (4, 2 or 1) at an address of the cluster's shared memory.
+template <int N>
+__device__ __forceinline__ void add_cluster_words(uint32_t (&c)[N], int n, uint32_t cluster_addr) {
+  uint32_t v[4] = {};
+  if (N >= 4 && n == 4)
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(cluster_addr) : "memory");
+  else if (N >= 2 && n == 2)
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(cluster_addr) : "memory");
+  else
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v[0]) : "r"(cluster_addr) : "memory");
+#pragma unroll
+  for (int x = 0; x < N; ++x) c[x] += v[x];
 }
-__device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, uint4 v) {
+__device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, const uint32_t (&v)[4]) {
   asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};"
-               :: "r"(cluster_addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+               :: "r"(cluster_addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 // Sum of the words before `below` of a warp-sized table (n <= 32 of them used), the same for every lane.
 __device__ __forceinline__ uint32_t sum_below(const uint32_t* table, int n, int below, int lane) {
@@ -175,31 +185,34 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) mla_select_kernel(const __grid
     // the bin of the need-th largest key: thread t owns `each` bins, counted from the top
     constexpr int MOST = SEL_BINS / SEL_THREADS;
     const int each = bins[d] / SEL_THREADS;              // 4, 2 or 1
-    uint32_t c[MOST] = {};
-    if (ncta == 1) {
+    const uint32_t first = bins[d] - (tid + 1) * each;   // the lowest of them
+    uint32_t c[MOST] = {};                               // the cluster's counts of bins first ..
+    if (ncta <= 4) {                                     // read from every CTA, all reads in flight together
 #pragma unroll
-      for (int x = 0; x < MOST; ++x)
-        if (x < each) c[x] = s.hist[d][bins[d] - 1 - (tid * each + x)];
+      for (uint32_t u = 0; u < 4; ++u)
+        if (u < ncta) add_cluster_words(c, each, ptx::mapa(ptx::smem_u32(&s.hist[d][first]), (rank + u) & (ncta - 1)));
     } else {
-      // four bins at a time, the CTAs' counts in flight together; each CTA begins with its own
-      const uint32_t slice = bins[d] / ncta;
-      for (uint32_t i = 4 * tid; i < slice; i += 4 * SEL_THREADS) {
-        const uint32_t from = ptx::smem_u32(&s.hist[d][rank * slice + i]), to = ptx::smem_u32(&s.total[rank * slice + i]);
-        uint4 sum = make_uint4(0, 0, 0, 0);
-        for (uint32_t q0 = 0; q0 < ncta; q0 += 4) {
-          uint4 v[4];
+      // CTA r adds up slice r of the bins and hands the sums to all: four lanes share four bins, each reading
+      // and writing a quarter of the CTAs (2 or 4)
+      const uint32_t slice = bins[d] / ncta;             // at most 256, a multiple of 32
+      if (tid < static_cast<int>(slice)) {
+        const uint32_t bin = rank * slice + (tid & ~3u), q0 = rank + (tid & 3u);
+        const uint32_t from = ptx::smem_u32(&s.hist[d][bin]), to = ptx::smem_u32(&s.total[bin]);
+        uint32_t sum[4] = {};
 #pragma unroll
-          for (uint32_t u = 0; u < 4; ++u)
-            v[u] = q0 + u < ncta ? ld_cluster_v4(ptx::mapa(from, (rank + q0 + u) & (ncta - 1))) : make_uint4(0, 0, 0, 0);
+        for (uint32_t u = 0; u < SEL_MAX_CLUSTER / 4; ++u)
+          if (4 * u < ncta) add_cluster_words(sum, 4, ptx::mapa(from, (q0 + 4 * u) & (ncta - 1)));
 #pragma unroll
-          for (uint32_t u = 0; u < 4; ++u) sum = make_uint4(sum.x + v[u].x, sum.y + v[u].y, sum.z + v[u].z, sum.w + v[u].w);
+        for (int x = 0; x < 4; ++x) {
+          sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
+          sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
         }
-        for (uint32_t q = 0; q < ncta; ++q) st_cluster_v4(ptx::mapa(to, (rank + q) & (ncta - 1)), sum);
+        for (uint32_t u = 0; 4 * u < ncta; ++u) st_cluster_v4(ptx::mapa(to, (q0 + 4 * u) & (ncta - 1)), sum);
       }
       ptx::cluster_sync();                               // every CTA holds the sums
 #pragma unroll
       for (int x = 0; x < MOST; ++x)
-        if (x < each) c[x] = s.total[bins[d] - 1 - (tid * each + x)];
+        if (x < each) c[x] = s.total[first + x];
     }
     uint32_t own = 0;
 #pragma unroll
@@ -213,9 +226,9 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) mla_select_kernel(const __grid
     __syncthreads();
     uint32_t above = inc - own + sum_below(s.scan, SEL_WARPS, warp, lane);
 #pragma unroll
-    for (int x = 0; x < MOST; ++x) {
-      if (x < each && above < need && need <= above + c[x]) {
-        s.bin = bins[d] - 1 - (tid * each + x);
+    for (int x = MOST - 1; x >= 0; --x) {                // (c[x] of bins that are not its own is 0)
+      if (above < need && need <= above + c[x]) {
+        s.bin = first + x;
         s.need = need - above;
       }
       above += c[x];
