@@ -459,6 +459,11 @@ def _check_scale_table(lookup_table, scales_lookup_table):
             raise ValueError("scales_lookup_table must have the shape of lookup_table")
 
 
+@functools.lru_cache(maxsize=1024)      # a function of the sizes alone, only read by the library
+def _shape_record(*sizes):
+    return PagedShape(*sizes)
+
+
 def _cache_shape(blocks, scales, scales_lookup_table, batch, heads, v_dim, lookup_table):
     """Shape record of a cache whose scales, where it has them, hold each token's in the last dim."""
     NB, KVD, NL, P, NKV, D = blocks.shape
@@ -469,7 +474,7 @@ def _cache_shape(blocks, scales, scales_lookup_table, batch, heads, v_dim, looku
             raise ValueError("scales must match blocks in kv_dim, num_layers, page_size and num_heads")
         if NSB != NB and scales_lookup_table is None:
             raise ValueError("without a scales_lookup_table, scales must have as many blocks as blocks")
-    return PagedShape(batch, heads, D, v_dim, NB, KVD, NL, P, NKV, NSB, g, lookup_table.shape[1])
+    return _shape_record(batch, heads, D, v_dim, NB, KVD, NL, P, NKV, NSB, g, lookup_table.shape[1])
 
 
 def _token_count(max_prompt_length, tokens):
@@ -619,7 +624,7 @@ def _check_mha(blocks, scales, cache_lengths, lookup_table, scales_lookup_table,
         if scales_lookup_table is None and NSB != NB:
             raise ValueError("without a scales_lookup_table, scales must have as many blocks as blocks")
     _check_tables(cache_lengths, lookup_table, scales_lookup_table, batch)
-    return PagedShape(batch, heads, D, D, NB, KVD, NL, P, NKV, NSB, 1, lookup_table.shape[1])
+    return _shape_record(batch, heads, D, D, NB, KVD, NL, P, NKV, NSB, 1, lookup_table.shape[1])
 
 
 def mha_kv_store(k, v, cache_lengths, lookup_table, scales_lookup_table, layer_idx: int, blocks, scales=None, stream=None):
