@@ -29,8 +29,13 @@
 // end to end are cut into equal contiguous ranges, one per CTA.  An item cut by a range's end leaves normalised fp32 partials
 // and their log-sum-exp in the workspace and a second kernel joins them; each CTA names the item whose
 // head it holds and the last CTA of it, so the join needs no plan and nothing has to start at zero.
-// Where all requests are short (one or two tiles), each CTA takes one item and the second launch is
+// Where all requests are short (up to four tiles), each CTA takes one item and the second launch is
 // left out.
+//
+// Measured (floor, the cache's bytes at the copy rate): 64 requests of 1 to 32k, 2 tokens, 32/8 heads of 128,
+// bf16 165 us (155), e4m3 97 (80); 128 of 8k, 64/8 heads of 128, e4m3 334 to 376 by machine (338); heads of 64,
+// e4m3 193 (174); 2 short requests 5.6.  Above 8 rows a head (16 here: 224, floor 170) and with one kv head (66,
+// floor 42) the latency of a warp's own chain shows, with two warps to a scheduler.
 #pragma once
 #include <cstdint>
 #include "mla_kernels.cuh"
