@@ -82,7 +82,7 @@ constexpr int ACC_MAX_WIDE = 12, ACC_MAX_NARROW = 4;   // slots of the two rings
 constexpr uint32_t ACC_WIDE_BYTES = ACC_BN * 128, ACC_NARROW_BYTES = ACC_BN * 64;
 // Shared memory: head factors, barriers, scalars; then q, each column [2 x heads rows (hi, then lo)], and
 // the rings in what is left (4 and 2 slots at 128 heads, up to 12 and 4 for few heads).
-constexpr uint32_t ACC_SH = 0;                    // [2][128] {factor, -lse log2 e}
+constexpr uint32_t ACC_SH = 0;                    // [2][64] {2^-k, 2^-k, -lse, -lse} of two heads
 constexpr uint32_t ACC_SBAR = ACC_SH + 2 * ACC_HEADS * 8;
 constexpr uint32_t ACC_SMISC = ACC_SBAR + 512;
 constexpr uint32_t ACC_SQ = 3 * 1024;
@@ -207,12 +207,13 @@ struct AccWalker {
 
 // The key a thread owns in tile j of request b: its place, its scale and its running sum.
 struct AccKey {
-  float scale, base;
+  float2 scale;                    // softmax_scale times the key's scale, and what that rounding left
+  float base;
   float* dst;                      // null: past the request's end, or in a page that does not exist
 };
 __device__ __forceinline__ AccKey acc_key(const AccumulateParams& p, int b, int item, int j, int r) {
   AccKey k;
-  k.scale = 0.f;
+  k.scale = make_float2(0.f, 0.f);
   k.base = 0.f;
   k.dst = nullptr;
   const uint32_t L = acc_length(p, b), t = static_cast<uint32_t>(j) * ACC_BN + r;
@@ -225,30 +226,39 @@ __device__ __forceinline__ AccKey acc_key(const AccumulateParams& p, int b, int 
     raise_status(p.status, STATUS_BOUNDS);
     return k;
   }
-  k.scale = p.scales[((static_cast<size_t>(sblk) * p.KVD) * p.NL + p.layer) * p.P + slot];
+  const float s = p.scales[((static_cast<size_t>(sblk) * p.KVD) * p.NL + p.layer) * p.P + slot];
+  k.scale.x = s * p.softmax_scale;
+  k.scale.y = fmaf(s, p.softmax_scale, -k.scale.x);
   k.dst = p.out + b * p.out_stride + t;
   if (item == 0 && p.i0 == 0 && p.scores && t < L) k.base = p.scores[b * p.scores_stride + t];
   return k;
 }
 
-// Sum over W heads: the thread's hi and lo columns, its scale, and each head's factor and -lse.
+// Sum over W heads, two at a time: the thread's hi and lo columns, its scale, and each pair's powers of two and
+// -lse.  A rounding of the score, relative to its size, would be a relative error of the weight several times
+// as large, the same for all heads or all keys where it is a factor's: so the factor has two terms, the score
+// meets the lse before it is rounded, and log2 e multiplies what is left.
 template <int W>
-__device__ __forceinline__ void acc_heads(const uint32_t (&hi)[W], const uint32_t (&lo)[W], float s, uint32_t hf,
-                                          float (&sum)[4]) {
+__device__ __forceinline__ void acc_heads(const uint32_t (&hi)[W], const uint32_t (&lo)[W], float2 s, uint32_t hf,
+                                          float2 (&sum)[2]) {
+  const float2 s0 = make_float2(s.x, s.x), s1 = make_float2(s.y, s.y);
 #pragma unroll
   for (int x = 0; x < W; x += 2) {
-    const uint4 f = ptx::ld_shared_v4(hf + x * 8);       // {factor, -lse} of two heads
-    const float x0 = fmaf(__uint_as_float(lo[x]), 0.0625f, __uint_as_float(hi[x])) * s;
-    const float x1 = fmaf(__uint_as_float(lo[x + 1]), 0.0625f, __uint_as_float(hi[x + 1])) * s;
-    sum[x & 2] += ptx::ex2_approx(fmaf(x0, __uint_as_float(f.x), __uint_as_float(f.y)));
-    sum[(x & 2) + 1] += ptx::ex2_approx(fmaf(x1, __uint_as_float(f.z), __uint_as_float(f.w)));
+    const uint4 f = ptx::ld_shared_v4(hf + x * 8);       // 2^-k of two heads, then their -lse
+    const float2 k = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
+    const float2 v = __ffma2_rn(make_float2(__uint_as_float(lo[x]), __uint_as_float(lo[x + 1])), make_float2(0.0625f, 0.0625f),
+                                make_float2(__uint_as_float(hi[x]), __uint_as_float(hi[x + 1])));
+    float2 e = __ffma2_rn(v, __fmul2_rn(k, s0), make_float2(__uint_as_float(f.z), __uint_as_float(f.w)));
+    e = __ffma2_rn(v, __fmul2_rn(k, s1), e);
+    e = __fmul2_rn(e, make_float2(1.4426950408889634f, 1.4426950408889634f));
+    sum[(x >> 1) & 1] = __fadd2_rn(sum[(x >> 1) & 1], make_float2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y)));
   }
 }
 
 // ------------------------------------------------------------------ q split
 // Workspace of an item ((b * ni + i) * G + g): 4 columns of 2 hpad rows (hi of each head, then lo) of
-// 128 bytes in the 128-byte swizzle, one of 64 bytes in the 64-byte swizzle, then {factor, -lse log2 e}
-// of each head; hpad heads, a multiple of 8.
+// 128 bytes in the 128-byte swizzle, one of 64 bytes in the 64-byte swizzle, then for every two heads the
+// powers of two that undo their scaling and their -lse; hpad heads, a multiple of 8.
 __device__ __forceinline__ uint32_t acc_hpad(const AccumulateParams& p, int g) {
   return (min(p.H - g * ACC_HEADS, ACC_HEADS) + 7) & ~7;
 }
@@ -310,13 +320,9 @@ __global__ void __launch_bounds__(256) mla_split_q_kernel(const __grid_constant_
   if (lane == 0) {
     // no such head, or a row without keys: weight 0.  A non-finite row gets a NaN factor (its codes
     // would saturate) and makes the request's sums NaN.
-    float2 hf = make_float2(0.f, -INFINITY);
-    if (lse != -INFINITY) {
-      hf.x = m >= 0x7F80u ? __uint_as_float(0x7FC00000u)
-                          : p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-      hf.y = -lse * 1.4426950408889634f;
-    }
-    reinterpret_cast<float2*>(dst + hpad * 2 * HEAD_DIM)[r] = hf;
+    float* hf = reinterpret_cast<float*>(dst + hpad * 2 * HEAD_DIM) + (r >> 1) * 4 + (r & 1);
+    hf[0] = lse == -INFINITY ? 0.f : m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+    hf[2] = lse == -INFINITY ? -INFINITY : -lse;
   }
 }
 
@@ -545,7 +551,7 @@ __global__ void __launch_bounds__(ACC_THREADS, 1) mla_accumulate_kernel(const __
     const uint32_t d = tbase + (static_cast<uint32_t>(warp & 3) << 21) + buf * 256;
     uint32_t use = 0, items = 0;
     bool live = w.start(p, t0);
-    AccKey key{0.f, 0.f, nullptr}, nxt{0.f, 0.f, nullptr};
+    AccKey key{}, nxt{};
     if (live && (w.j & 1) == static_cast<int>(buf)) key = acc_key(p, w.b, w.item, w.j, r);
     while (live) {
       const AccWalker cur = w;
@@ -563,7 +569,7 @@ __global__ void __launch_bounds__(ACC_THREADS, 1) mla_accumulate_kernel(const __
         if (!__all_sync(0xffffffffu, wait(bar(AB_ACC_FULL + buf), use & 1))) break;
         ++use;
         ptx::tc_fence_after();
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         uint32_t h = 0;
         for (; h + 32 <= hpad; h += 32) {
           uint32_t hi[32], lo[32];
@@ -583,7 +589,7 @@ __global__ void __launch_bounds__(ACC_THREADS, 1) mla_accumulate_kernel(const __
         ptx::mbar_arrive(bar(AB_ACC_EMPTY + buf));
         if (key.dst) {
           const uint32_t t = static_cast<uint32_t>(cur.j) * ACC_BN + r;
-          const float add = t <= acc_length(p, cur.b) + p.i0 + i ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
+          const float add = t <= acc_length(p, cur.b) + p.i0 + i ? (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y) : 0.f;
           *key.dst = (cur.item == 0 && p.i0 == 0 ? key.base : *key.dst) + add;
         }
       }
