@@ -437,8 +437,9 @@ mla_status_t mla_mha_kv_store(
  *     lse  = ln sum_t exp(x[t]),  out[b,i,h,:] = sum_t exp(x[t] - lse) V[t],
  * with K and V the stored bf16 values, or e4m3 * scale unrounded.  Keys, values and scales of the
  * stored tokens are to be finite; what the cache holds behind a request's end is never used.  Weights are
- * rounded to bf16, or for e4m3 to 11 bits with V's scale folded in: all 11 while V's scale is above 2^-23 of
- * the largest of the request and head (rows of zeros included, whose scale mla_mha_kv_store sets to 1).
+ * held as two bf16 terms (16 bits), or for e4m3 in 11 bits with V's scale folded in: all 11 while V's scale is
+ * above 2^-23 of the largest of the request and head (rows of zeros included, whose scale mla_mha_kv_store
+ * sets to 1).
  *
  *   q          bf16 [batch, max_prompt_length, num_q_heads, head_dim], 16-byte aligned
  *   out        bf16, as q, not overlapping it; lse fp32 [batch, max_prompt_length, num_q_heads], natural log, or NULL

@@ -19,16 +19,20 @@
 // ninth warp keeps a ring of tiles full by TMA: one box per page run and plane, [column of 128 (64)
 // bytes][key], in the matching shared-memory swizzle, so that ldmatrix reads rows without bank conflicts.
 //
+// The weights enter the value product as two bf16 terms for a bf16 cache: one alone would add as much error as
+// the rounding of the output, and the second costs nothing that shows (165 us with and without it, below).
+//
 // e4m3.  The values are converted to f16, exactly, as they leave shared memory (two per instruction),
 // and never to anything wider: q is brought to f16 with a power of two (exact down to 2^-30 of the
 // largest value), K's scale multiplies the score, and V's scale goes into the weight, relative to a
-// running power-of-two bound of V's scales so that f16 holds it with 11 bits (down to 2^-23 of the bound).  The instructions of this
-// are what keeps an e4m3 cache from the copy rate: the loads alone run at it.
+// running power-of-two bound of V's scales so that f16 holds it with 11 bits (down to 2^-23 of the bound).
+// The instructions of this are what keeps an e4m3 cache from the copy rate: the loads alone run at it.
 //
 // Work split.  The tiles of all (request, head group, row group) items, with each item's fixed cost, laid
-// end to end are cut into equal contiguous ranges, one per CTA.  An item cut by a range's end leaves normalised fp32 partials
-// and their log-sum-exp in the workspace and a second kernel joins them; each CTA names the item whose
-// head it holds and the last CTA of it, so the join needs no plan and nothing has to start at zero.
+// end to end are cut into equal contiguous ranges, one per CTA.  An item cut by a range's end leaves
+// normalised fp32 partials and their log-sum-exp in the workspace and a second kernel joins them; each CTA
+// names the item whose head it holds and the last CTA of it, so the join needs no plan and nothing has to
+// start at zero.
 // Where all requests are short (up to four tiles), each CTA takes one item and the second launch is
 // left out.
 //
@@ -294,7 +298,8 @@ struct MhaRows {
     }
   }
 
-  // Scores to weights (pb: B fragments of the value product) against a reference maximum that trails the
+  // Scores to weights (pb: B fragments of the value product; for a bf16 cache, whose 8 bits would be the
+  // largest error before the output's rounding, pl: what that rounding left, multiplied as well) against a reference maximum that trails the
   // running one by at most LAZY (log2): weights stay below 2^LAZY and O is rescaled rarely.  ks, vs: the
   // scales of the step's first key, sstep bytes from key to key; key0: the first key, n: stored keys.
   static constexpr float LAZY = 6.f;
@@ -304,7 +309,7 @@ struct MhaRows {
   static constexpr int VSHIFT = 9;
   template <int KS>
   __device__ __forceinline__ void weights(const MhaParams& p, float2 (&s)[KS][NR][2], uint32_t ks, uint32_t vs, uint32_t sstep,
-                                          uint32_t key0, uint32_t n, int lane, uint32_t (&pb)[KS][NR][2]) {
+                                          uint32_t key0, uint32_t n, int lane, uint32_t (&pb)[KS][NR][2], uint32_t (&pl)[KS][NR][2]) {
     const int g = lane >> 2;
     float sv[KS][2];
     if (FP8) {
@@ -397,7 +402,9 @@ struct MhaRows {
             w = __fmul2_rn(w, make_float2(f, f));
             pb[y][u][x] = transpose8(ptx::pack_f16x2(w.x, w.y));
           } else {
-            pb[y][u][x] = transpose8(ptx::pack_bf16x2(w.x, w.y));
+            const uint32_t h = ptx::pack_bf16x2(w.x, w.y);
+            pb[y][u][x] = transpose8(h);
+            pl[y][u][x] = transpose8(ptx::pack_bf16x2(w.x - __uint_as_float(h << 16), w.y - __uint_as_float(h & 0xFFFF0000u)));
           }
         }
     }
@@ -405,7 +412,8 @@ struct MhaRows {
 
   // O^T += V^T P^T; vcol, pitch as for scores.
   template <int KS>
-  __device__ __forceinline__ void values(uint32_t vcol, uint32_t pitch, const uint32_t (&pb)[KS][NR][2]) {
+  __device__ __forceinline__ void values(uint32_t vcol, uint32_t pitch, const uint32_t (&pb)[KS][NR][2],
+                                         const uint32_t (&pl)[KS][NR][2]) {
     const uint32_t a0 = vcol + voff, a1 = a0 + pitch;
     if (!FP8) {
 #pragma unroll
@@ -415,7 +423,10 @@ struct MhaRows {
           uint32_t a[4];
           ldsm4_t(((k * 32 < CW ? a0 : a1) ^ ((k * 32) % CW)) + y * 16 * CW, a);
 #pragma unroll
-          for (int u = 0; u < NR; ++u) mma_16816<false>(o[k][u][0], o[k][u][1], a, pb[y][u][0], pb[y][u][1]);
+          for (int u = 0; u < NR; ++u) {
+            mma_16816<false>(o[k][u][0], o[k][u][1], a, pb[y][u][0], pb[y][u][1]);
+            mma_16816<false>(o[k][u][0], o[k][u][1], a, pl[y][u][0], pl[y][u][1]);
+          }
         }
     } else {
 #pragma unroll
@@ -696,8 +707,8 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
         for (uint32_t g = g0; g < static_cast<uint32_t>(p.tile) && live; g += gstep) {
           const bool end = g + gstep >= static_cast<uint32_t>(p.tile);   // this warp's last step of the tile
           const bool more = !end || j + 1 < u.tb;
-          uint32_t pb[KS][NR][2];
-          if (cur.ok) w.template weights<KS>(p, s, cur.sc, cur.sc + vscales, sstep, cur.key0, stored, lane, pb);
+          uint32_t pb[KS][NR][2], pl[KS][NR][2];
+          if (cur.ok) w.template weights<KS>(p, s, cur.sc, cur.sc + vscales, sstep, cur.key0, stored, lane, pb, pl);
           if (end) {
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(empty_k(stk));   // the tile's K and scales are read
@@ -721,7 +732,7 @@ __global__ void __launch_bounds__(MHA_THREADS, 1) mla_mha_decode_kernel(const __
             }
             // (the last step of a piece forms its own scores again: nothing reads them)
             w.template scores<KS>(nxt.k, pitch, s);
-            w.template values<KS>(v, pitch, pb);
+            w.template values<KS>(v, pitch, pb, pl);
           } else if (nxt.ok) {
             w.template scores<KS>(nxt.k, pitch, s);
           }

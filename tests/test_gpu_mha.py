@@ -2,7 +2,7 @@
 
 Tolerances.  Scores: fp32 sums of D products, (D + 8) 2^-24 of the sum of magnitudes A, plus the
 exponent's roundings; an error e of every score moves a weight by at most a factor exp(2 e).  Weights
-are rounded to bf16 (half a step, 2^-8) for a bf16 cache, to f16 (2^-11, and 2^-25 of V's scale bound
+are two bf16 terms (half a step, 2^-8, of half a step) for a bf16 cache, rounded to f16 (2^-11, and 2^-25 of V's scale bound
 below its normal range: at most twice the largest scale, times 448, per key) for an e4m3 cache; the
 output is rounded to bf16 (2^-8).  The log-sum-exp has the scores' error and its own fp32 roundings."""
 import pytest
@@ -31,7 +31,7 @@ def check(cache, q, lengths, scale, out, lse, only=None):
         ro, rl, mag, amp = mha_reference(cache, b, q[b], L, scale)
         n, D = L + q.shape[1], q.shape[-1]
         e = (D + 8) * U * amp + 8 * U * (rl.abs() + amp) + 2.0 ** -21
-        weight = 2.0 ** -11 if cache.fp8 else 2.0 ** -8
+        weight = 2.0 ** -11 if cache.fp8 else 2.0 ** -16
         tol = mag * (weight + 2 * e[..., None] + (n + 64) * U) + ro.abs() * 2.0 ** -8
         if cache.fp8:
             # f16 weights below the normal range: 2^-25 of V's scale bound per key, times the code (448)
