@@ -436,7 +436,8 @@ mla_status_t mla_mha_kv_store(
  *     x[t] = softmax_scale <q[b,i,h,:], K[t]> for t <= cache_lengths[b] + i,
  *     lse  = ln sum_t exp(x[t]),  out[b,i,h,:] = sum_t exp(x[t] - lse) V[t],
  * with K and V the stored bf16 values, or e4m3 * scale unrounded.  Keys, values and scales of the
- * stored tokens are to be finite; what the cache holds behind a request's end is never used.  Weights are
+ * stored tokens are to be finite; what the cache holds behind a request's end is never used.  A query row
+ * with an infinity or a NaN makes its own out and lse NaN and no other's.  Weights are
  * held as two bf16 terms (16 bits), or for e4m3 in 11 bits with V's scale folded in: all 11 while V's scale is
  * above 2^-23 of the largest of the request and head (rows of zeros included, whose scale mla_mha_kv_store
  * sets to 1).

@@ -23,10 +23,12 @@
 // the rounding of the output, and the second costs nothing that shows (165 us with and without it, below).
 //
 // e4m3.  The values are converted to f16, exactly, as they leave shared memory (two per instruction),
-// and never to anything wider: q is brought to f16 with a power of two (exact down to 2^-30 of the
-// largest value), K's scale multiplies the score, and V's scale goes into the weight, relative to a
+// and never to anything wider: each row of q is brought to f16 with a power of two of its own (exact down to
+// 2^-30 of the row's largest value, and no row depends on those beside it), K's scale multiplies the score, and V's scale goes into the weight, relative to a
 // running power-of-two bound of V's scales so that f16 holds it with 11 bits (down to 2^-23 of the bound).
-// The instructions of this are what keeps an e4m3 cache from the copy rate: the loads alone run at it.
+// The instructions of this are what keeps an e4m3 cache from the copy rate: the loads alone run at it.  (One power
+// of two for a warp's rows together cost nothing elsewhere, but took 130 instead of 140 us for 64 requests of 8k, 16
+// rows a head of 64; a row's infinity, NaN or much larger values then spoilt its neighbours'.)
 //
 // Work split.  The tiles of all (request, head group, row group) items, with each item's fixed cost, laid
 // end to end are cut into equal contiguous ranges, one per CTA.  An item cut by a range's end leaves
@@ -191,7 +193,7 @@ struct MhaRows {
   float m[NR][2];                  // reference maxima (base 2) of rows 2t, 2t + 1
   float2 l[NR];                    // this thread's part of their sums
   uint32_t last[NR][2];            // their last visible keys
-  float xs;                        // score factor
+  float2 xs[FP8 ? NR : 1];         // score factors: of rows 2t and 2t + 1, or the one of all rows
   float vref;                      // e4m3: power-of-two bound of V's scales so far (0: none yet)
   uint32_t koff, voff;             // this lane's place in a 16-key block of K and V
 
@@ -199,13 +201,14 @@ struct MhaRows {
   static __device__ __forceinline__ int dim_a(int k, int g) { return 16 * k + (FP8 ? 2 * g : g); }
   static __device__ __forceinline__ int dim_b(int k, int g) { return 16 * k + (FP8 ? 2 * g + 1 : g + 8); }
 
-  // Query rows row0 .. row0 + 8 NR - 1 of kv head kvh (rows past the last one are zero).  For e4m3 caches q
-  // is brought to f16 by one power of two for the warp's rows (largest value into [2^12, 2^13)).
+  // Query rows row0 .. row0 + 8 NR - 1 of kv head kvh (rows past the last one are zero).  For e4m3 caches each
+  // row is brought to f16 by a power of two (its largest value into [2^12, 2^13)).
   __device__ __forceinline__ void load_q(const MhaParams& p, int b, int kvh, int row0, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    uint32_t m2 = 0;
+    if (!FP8) xs[0] = make_float2(p.scale_log2, p.scale_log2);
 #pragma unroll
     for (int u = 0; u < NR; ++u) {
+      uint32_t m2 = 0;
       const int r = row0 + 8 * u + g;
       const bool have = r < p.R;
       const int i = have ? static_cast<int>(p.divG.div(r)) : 0;
@@ -230,20 +233,19 @@ struct MhaRows {
         m[u][e] = -INFINITY;
       }
       l[u] = make_float2(0.f, 0.f);
-    }
-    xs = p.scale_log2;
-    if (FP8) {
-      const uint32_t big = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
-      const int e = big == 0 ? 0 : min(max(12 - (static_cast<int>(big >> 7) - 127), -115), 126);
-      const float f = pow2(e);
-      xs = big >= 0x7F80u ? __uint_as_float(0x7FC00000u) : p.scale_log2 * pow2(-e);
-#pragma unroll
-      for (int u = 0; u < NR; ++u)
+      if (FP8) {                                         // row g lies in the four lanes of g, its scores in those of t = g / 2
+        uint32_t big = max(m2 & 0xFFFFu, m2 >> 16);
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const int e = big == 0 ? 0 : min(max(12 - (static_cast<int>(big >> 7) - 127), -115), 126);
+        const float f = pow2(e), own = big >= 0x7F80u ? __uint_as_float(0x7FC00000u) : p.scale_log2 * pow2(-e);
+        xs[u] = make_float2(__shfl_sync(0xffffffffu, own, 8 * t), __shfl_sync(0xffffffffu, own, 8 * t + 4));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
             qb[u][k][x] = ptx::pack_f16x2(__uint_as_float(qb[u][k][x] << 16) * f, __uint_as_float(qb[u][k][x] & 0xFFFF0000u) * f);
+      }
     }
 #pragma unroll
     for (int k = 0; k < D / 16; ++k)
@@ -320,15 +322,16 @@ struct MhaRows {
     for (int y = 0; y < KS; ++y)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {     // key 16 y + 8 x + g
-        float f = xs;
+        float kf = 1.f;
         if (FP8) {
-          f *= ptx::ld_shared_f32(ks);
+          kf = ptx::ld_shared_f32(ks);
           sv[y][x] = ptx::ld_shared_f32(vs);
           ks += 8 * sstep;
           vs += 8 * sstep;
         }
 #pragma unroll
-        for (int u = 0; u < NR; ++u) s[y][u][x] = __fmul2_rn(s[y][u][x], make_float2(f, f));
+        for (int u = 0; u < NR; ++u)
+          s[y][u][x] = __fmul2_rn(s[y][u][x], FP8 ? make_float2(xs[FP8 ? u : 0].x * kf, xs[FP8 ? u : 0].y * kf) : xs[0]);
       }
     if (key0 + 16 * KS - 1 > n - p.T) {   // some row may not see some of the keys
 #pragma unroll
