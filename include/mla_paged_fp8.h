@@ -459,7 +459,8 @@ mla_status_t mla_mha_decode_paged(
     int32_t element_bytes, const mla_paged_shape_t* shape, void* out, float* lse,
     void* workspace, uint64_t workspace_bytes, cudaStream_t stream);
 
-/* Bytes of workspace that mla_mha_decode_paged needs for these arguments on the current device. */
+/* Bytes of workspace that mla_mha_decode_paged needs for these arguments on the current device.  Refuses the shapes
+ * and element_bytes that the call refuses. */
 mla_status_t mla_mha_decode_workspace_bytes(
     uint32_t max_prompt_length, uint32_t max_cache_length, int32_t element_bytes,
     const mla_paged_shape_t* shape, uint64_t* bytes);

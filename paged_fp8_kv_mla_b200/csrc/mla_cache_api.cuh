@@ -104,17 +104,11 @@ mla_status_t check_pages(const mla_paged_shape_t* s, uint32_t layer_idx) {
 
 // The multi-head cache: kv plane 0 keys, plane 1 values, head_dim 64 or 128, bf16 or e4m3 with one scale
 // per token and head.
-mla_status_t check_mha(const mla_paged_shape_t* s, uint32_t layer_idx, int32_t element_bytes, const void* blocks,
-                       const void* scales, const uint32_t* cache_lengths, const uint32_t* lookup_table) {
-  if (!s) return fail(MLA_ERR_INVALID_ARG, "shape is NULL");
-  if (!blocks || !cache_lengths || !lookup_table)
-    return fail(MLA_ERR_INVALID_ARG, "blocks, cache_lengths and lookup_table must be non-NULL");
+mla_status_t check_mha_shape(const mla_paged_shape_t* s, uint32_t layer_idx, int32_t element_bytes) {
   const mla_status_t st = check_pages(s, layer_idx);
   if (st != MLA_OK) return st;
   if (element_bytes != 1 && element_bytes != 2)
     return fail(MLA_ERR_INVALID_ARG, "element_bytes must be 1 (e4m3) or 2 (bf16), got %d", element_bytes);
-  if ((element_bytes == 1) != (scales != nullptr))
-    return fail(MLA_ERR_INVALID_ARG, "an e4m3 cache needs scales and a bf16 cache takes none");
   if (s->head_dim != 64 && s->head_dim != 128)
     return fail(MLA_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", s->head_dim);
   if (s->kv_dim < 2) return fail(MLA_ERR_INVALID_ARG, "kv_dim must be at least 2 (keys and values)");
@@ -122,6 +116,18 @@ mla_status_t check_mha(const mla_paged_shape_t* s, uint32_t layer_idx, int32_t e
   if (s->head_dim_granularity != 1)
     return fail(MLA_ERR_UNSUPPORTED, "only one scale per token and head (head_dim_granularity 1) is implemented");
   if (s->page_size % 16 != 0) return fail(MLA_ERR_UNSUPPORTED, "page_size must be a multiple of 16");
+  return MLA_OK;
+}
+
+mla_status_t check_mha(const mla_paged_shape_t* s, uint32_t layer_idx, int32_t element_bytes, const void* blocks,
+                       const void* scales, const uint32_t* cache_lengths, const uint32_t* lookup_table) {
+  if (!s) return fail(MLA_ERR_INVALID_ARG, "shape is NULL");
+  if (!blocks || !cache_lengths || !lookup_table)
+    return fail(MLA_ERR_INVALID_ARG, "blocks, cache_lengths and lookup_table must be non-NULL");
+  const mla_status_t st = check_mha_shape(s, layer_idx, element_bytes);
+  if (st != MLA_OK) return st;
+  if ((element_bytes == 1) != (scales != nullptr))
+    return fail(MLA_ERR_INVALID_ARG, "an e4m3 cache needs scales and a bf16 cache takes none");
   if (!aligned16(blocks) || !aligned16(scales)) return fail(MLA_ERR_INVALID_ARG, "blocks and scales must be 16-byte aligned");
   return MLA_OK;
 }
@@ -595,14 +601,15 @@ mla_status_t mla_mha_decode_workspace_bytes(uint32_t max_prompt_length, uint32_t
                                             const mla_paged_shape_t* s, uint64_t* bytes) {
   if (!s || !bytes) return fail(MLA_ERR_INVALID_ARG, "shape and bytes must be non-NULL");
   *bytes = 0;
-  mla_status_t st = check_pages(s, 0);
+  mla_status_t st = check_mha_shape(s, 0, element_bytes);
   if (st != MLA_OK) return st;
-  if (s->batch == 0) return MLA_OK;
+  MhaPlan m{};                                           // what it refuses does not depend on the device
+  st = mha_plan(s, max_prompt_length, max_cache_length, element_bytes, 1, &m);
+  if (st != MLA_OK || s->batch == 0) return st;
   int sms = 0;
   unsigned int* status = nullptr;
   st = cache_device(&sms, &status);
   if (st != MLA_OK) return st;
-  MhaPlan m{};
   st = mha_plan(s, max_prompt_length, max_cache_length, element_bytes, sms, &m);
   if (st == MLA_OK) *bytes = m.total;
   return st;
