@@ -283,10 +283,13 @@ __global__ void __launch_bounds__(256) mla_split_q_kernel(const __grid_constant_
   const uint4* src = reinterpret_cast<const uint4*>(p.q + row * HEAD_DIM);
   const float lse = have ? p.lse[row] : -INFINITY;
   uint4 v[3];
+#pragma unroll
+  for (int c = 0; c < 3; ++c)
+    v[c] = have && lane + 32 * c < HEAD_DIM / 8 ? src[lane + 32 * c] : make_uint4(0, 0, 0, 0);
   uint32_t m2 = 0;
 #pragma unroll
   for (int c = 0; c < 3; ++c) {
-    v[c] = have && lane + 32 * c < HEAD_DIM / 8 ? src[lane + 32 * c] : make_uint4(0, 0, 0, 0);
+    if (lse == -INFINITY) v[c] = make_uint4(0, 0, 0, 0);   // adds nothing, whatever it holds (a padded token)
     m2 = __vmaxu2(__vmaxu2(m2, v[c].x & 0x7FFF7FFFu), v[c].y & 0x7FFF7FFFu);
     m2 = __vmaxu2(__vmaxu2(m2, v[c].z & 0x7FFF7FFFu), v[c].w & 0x7FFF7FFFu);
   }

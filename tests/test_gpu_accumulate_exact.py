@@ -70,3 +70,17 @@ def test_weights_of_exact_products(H, power, depth):
     got = run(cache, q, lse[None, None], n, scores)[0]
     bad = ~((got - total).abs() <= tol)
     assert not bad.any(), (bad.nonzero()[:5].T, got[bad][:5], total[bad][:5], tol[bad][:5])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_a_row_whose_lse_is_minus_infinity_adds_nothing_whatever_it_holds(value):
+    """A padded query token: q was never written, and its lse says that it attends to nothing."""
+    n, H = 200, 16
+    cache, q, gen = build(n, H, 3)
+    lse = torch.full((1, 1, H), 1000.0)
+    scores = torch.rand((1, n), generator=gen)
+    lse[0, 0, 4] = lse[0, 0, 9] = float("-inf")
+    want = run(cache, q, lse, n, scores)
+    q[0, 0, 4, 7] = value
+    q[0, 0, 9] = value
+    assert torch.equal(run(cache, q, lse, n, scores), want)
