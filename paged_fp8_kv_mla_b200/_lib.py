@@ -477,6 +477,17 @@ def _cache_shape(blocks, scales, scales_lookup_table, batch, heads, v_dim, looku
     return _shape_record(batch, heads, D, v_dim, NB, KVD, NL, P, NKV, NSB, g, lookup_table.shape[1])
 
 
+# ctypes wraps a number that its 32-bit argument does not hold: (n + _HALF) >> 32 is 0 for those it does.  (What is
+# left of the range is the library's to check.)
+_HALF, _MOST = 0x80000000, 0x7FFFFFFF
+
+
+def _too_wide(**numbers):
+    for name, n in numbers.items():
+        if (n + _HALF) >> 32:
+            raise ValueError(f"{name} does not fit 32 bits (got {n})")
+
+
 def _token_count(max_prompt_length, tokens):
     if max_prompt_length != tokens:
         raise ValueError(f"max_prompt_length must be q's number of tokens, {tokens} (got {max_prompt_length})")
@@ -504,6 +515,9 @@ def accumulate_weights(q, lse, blocks, scales, cache_lengths, lookup_table, scal
         _expect("scales", scales, (_F32,), ndim=6)
     _check_tables(cache_lengths, lookup_table, scales_lookup_table, B)
     _token_count(max_prompt_length, T)
+    max_cache_length, layer_idx = int(max_cache_length), int(layer_idx)
+    if (max_cache_length + _HALF | layer_idx + _HALF) >> 32:
+        _too_wide(max_cache_length=max_cache_length, layer_idx=layer_idx)
     shp = _cache_shape(blocks, scales, scales_lookup_table, B, H, 512, lookup_table)
     need = max_cache_length + T
     sstep = 0 if scores is None else _rows("scores", scores, _F32, B, need)
@@ -526,7 +540,7 @@ def accumulate_weights(q, lse, blocks, scales, cache_lengths, lookup_table, scal
     if workspace is None:
         workspace = _scratch(accumulate_workspace_bytes(B, T, H), q, dev, stream)
     _run(dev, lib.mla_accumulate_weights_fp8, q.data_ptr(), lse.data_ptr(), blocks.data_ptr(), scales.data_ptr(),
-         cache_lengths.data_ptr(), lookup_table.data_ptr(), _adr(scales_lookup_table), T, int(max_cache_length), int(layer_idx),
+         cache_lengths.data_ptr(), lookup_table.data_ptr(), _adr(scales_lookup_table), T, max_cache_length, layer_idx,
          float(softmax_scale), ctypes.byref(shp), _adr(scores), sstep, out.data_ptr(), ostep, _adr(workspace),
          0 if workspace is None else workspace.numel(), _raw_stream(stream, dev))
     return out
@@ -535,6 +549,8 @@ def accumulate_weights(q, lse, blocks, scales, cache_lengths, lookup_table, scal
 @functools.lru_cache(maxsize=1024)      # a function of the sizes alone
 def accumulate_workspace_bytes(batch: int, max_prompt_length: int, num_q_heads: int) -> int:
     """Bytes of workspace that accumulate_weights needs."""
+    if (batch + _HALF | max_prompt_length + _HALF | num_q_heads + _HALF) >> 32:
+        _too_wide(batch=batch, max_prompt_length=max_prompt_length, num_q_heads=num_q_heads)
     n, shp = ctypes.c_uint64(0), PagedShape(batch, num_q_heads)
     _check(load().mla_accumulate_workspace_bytes(max_prompt_length, ctypes.byref(shp), ctypes.byref(n)))
     return n.value
@@ -552,6 +568,9 @@ def select_keys(scores, lengths, max_length: int, budget: int, num_recent: int =
     if not _plain(lengths, _I32, 1):
         _expect("lengths", lengths, _U32, ndim=1)
     B = lengths.shape[0]
+    max_length, budget, num_recent, num_sink = int(max_length), int(budget), int(num_recent), int(num_sink)
+    if (max_length + _HALF | budget + _HALF | num_recent + _HALF | num_sink + _HALF) >> 32:
+        _too_wide(max_length=max_length, budget=budget, num_recent=num_recent, num_sink=num_sink)
     sstep = _rows("scores", scores, _F32, B, max_length)
     kstep = 0 if kept is None else _rows("kept", kept, _I32, B, min(budget, max_length))
     if kept_lengths is not None and (not _plain(kept_lengths, _I32, 1) or kept_lengths.shape[0] != B):
@@ -567,8 +586,8 @@ def select_keys(scores, lengths, max_length: int, budget: int, num_recent: int =
                 kept_lengths = torch.empty(B, dtype=_I32, device=scores.device)
     if B == 0:
         return kept, kept_lengths
-    _run(dev, lib.mla_select_keys, scores.data_ptr(), sstep, lengths.data_ptr(), B, int(max_length), int(budget),
-         int(num_recent), int(num_sink), kept.data_ptr(), kstep, kept_lengths.data_ptr(), _raw_stream(stream, dev))
+    _run(dev, lib.mla_select_keys, scores.data_ptr(), sstep, lengths.data_ptr(), B, max_length, budget,
+         num_recent, num_sink, kept.data_ptr(), kstep, kept_lengths.data_ptr(), _raw_stream(stream, dev))
     return kept, kept_lengths
 
 
@@ -591,14 +610,17 @@ def compact_cache(kept, kept_lengths, lookup_table, scales_lookup_table, layer_i
         raise ValueError(f"lookup_table must have {B} rows (one per request)")
     _check_scale_table(lookup_table, scales_lookup_table)
     kstep = _rows("kept", kept, _I32, B, 1)
+    layer_idx = int(layer_idx)
+    if (layer_idx + _HALF) >> 32:
+        _too_wide(layer_idx=layer_idx)
     shp = _cache_shape(blocks, scales, scales_lookup_table, B, 0, 0, lookup_table)
     sstep = 0 if scores is None else _rows("scores", scores, _F32, B, 1)
     dev = _one_device(kept, kept_lengths, lookup_table, scales_lookup_table, blocks, scales, scores)
     if B == 0:
         return blocks, scales, scores
-    _run(dev, load().mla_compact_paged, kept.data_ptr(), kstep, kept.shape[1], kept_lengths.data_ptr(),
-         lookup_table.data_ptr(), _adr(scales_lookup_table), int(layer_idx), blocks.element_size(), ctypes.byref(shp),
-         blocks.data_ptr(), _adr(scales), _adr(scores), sstep, 0 if scores is None else scores.shape[1],
+    _run(dev, load().mla_compact_paged, kept.data_ptr(), kstep, min(kept.shape[1], _MOST), kept_lengths.data_ptr(),
+         lookup_table.data_ptr(), _adr(scales_lookup_table), layer_idx, blocks.element_size(), ctypes.byref(shp),
+         blocks.data_ptr(), _adr(scales), _adr(scores), sstep, 0 if scores is None else min(scores.shape[1], _MOST),
          _raw_stream(stream, dev))
     return blocks, scales, scores
 
@@ -637,12 +659,15 @@ def mha_kv_store(k, v, cache_lengths, lookup_table, scales_lookup_table, layer_i
     B, T, HKV, D = k.shape
     if v.shape != k.shape:
         raise ValueError("k and v must have the same shape")
+    layer_idx = int(layer_idx)
+    if (layer_idx + _HALF) >> 32:
+        _too_wide(layer_idx=layer_idx)
     shp = _check_mha(blocks, scales, cache_lengths, lookup_table, scales_lookup_table, B, 0, HKV, D)
     dev = _one_device(k, v, blocks, scales, cache_lengths, lookup_table, scales_lookup_table)
     if B == 0 or T == 0:
         return blocks, scales
     _run(dev, load().mla_mha_kv_store, k.data_ptr(), v.data_ptr(), cache_lengths.data_ptr(), lookup_table.data_ptr(),
-         _adr(scales_lookup_table), T, int(layer_idx), blocks.element_size(), ctypes.byref(shp), blocks.data_ptr(), _adr(scales),
+         _adr(scales_lookup_table), T, layer_idx, blocks.element_size(), ctypes.byref(shp), blocks.data_ptr(), _adr(scales),
          _raw_stream(stream, dev))
     return blocks, scales
 
@@ -661,6 +686,9 @@ def mha_decode(q, blocks, scales, cache_lengths, lookup_table, scales_lookup_tab
         _expect("q", q, (_BF16,), ndim=4)
     B, T, H, D = q.shape
     _token_count(max_prompt_length, T)
+    max_cache_length, layer_idx = int(max_cache_length), int(layer_idx)
+    if (max_cache_length + _HALF | layer_idx + _HALF) >> 32:
+        _too_wide(max_cache_length=max_cache_length, layer_idx=layer_idx)
     shp = _check_mha(blocks, scales, cache_lengths, lookup_table, scales_lookup_table, B, H, 0, D)
     if out is not None and (not _plain(out, _BF16, 4) or out.shape != q.shape):
         raise ValueError(f"out must be a contiguous bf16 tensor of shape {tuple(q.shape)}")
@@ -679,10 +707,10 @@ def mha_decode(q, blocks, scales, cache_lengths, lookup_table, scales_lookup_tab
     if B == 0:
         return out, lse
     if workspace is None:
-        workspace = _scratch(_mha_workspace(dev, T, int(max_cache_length), blocks.element_size(), B, H, D, shp.num_kv_heads,
+        workspace = _scratch(_mha_workspace(dev, T, max_cache_length, blocks.element_size(), B, H, D, shp.num_kv_heads,
                                             shp.page_size, shp.max_pages), q, dev, stream)
     _run(dev, lib.mla_mha_decode_paged, q.data_ptr(), blocks.data_ptr(), _adr(scales), cache_lengths.data_ptr(),
-         lookup_table.data_ptr(), _adr(scales_lookup_table), T, int(max_cache_length), int(layer_idx), float(softmax_scale),
+         lookup_table.data_ptr(), _adr(scales_lookup_table), T, max_cache_length, layer_idx, float(softmax_scale),
          blocks.element_size(), ctypes.byref(shp), out.data_ptr(), _adr(lse), _adr(workspace),
          0 if workspace is None else workspace.numel(), _raw_stream(stream, dev))
     return out, lse
@@ -699,7 +727,10 @@ def _mha_workspace(device, T, max_cache_length, element_bytes, B, H, D, HKV, P, 
 def mha_decode_workspace_bytes(q, blocks, lookup_table, max_cache_length: int) -> int:
     """Bytes of workspace that mha_decode needs for these tensors (0 for short caches)."""
     B, T, H, D = q.shape
-    return _mha_workspace(q.get_device(), T, int(max_cache_length), blocks.element_size(), B, H, D, blocks.shape[4],
+    max_cache_length = int(max_cache_length)
+    if (max_cache_length + _HALF) >> 32:
+        _too_wide(max_cache_length=max_cache_length)
+    return _mha_workspace(q.get_device(), T, max_cache_length, blocks.element_size(), B, H, D, blocks.shape[4],
                           blocks.shape[3], lookup_table.shape[1])
 
 
