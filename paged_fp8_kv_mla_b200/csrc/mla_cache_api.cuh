@@ -217,6 +217,7 @@ mla_status_t mha_plan(const mla_paged_shape_t* s, uint32_t T, uint32_t max_cache
   while (m.tile < 128 && 2 * m.tile * per_key <= 73728) m.tile *= 2;
   m.box_rows = gcd_int(s->page_size, m.tile);
   if (m.box_rows > 256) m.box_rows = 256;                // (both are powers of two) a box's largest extent
+  // (at most 8 boxes to a tile: a box holds at least 16 keys, 16 ks where ks > 1, or 256 of a tile's at most 512)
   m.plane_bytes = static_cast<uint32_t>(m.tile) * m.hg * s->head_dim * element_bytes;
   m.stage_bytes = static_cast<uint32_t>(align_up(m.tile * per_key, 1024));
   const uint32_t merge = m.kw > 1 ? (s->head_dim == 64 ? mla::mha_merge_bytes<64>() : mla::mha_merge_bytes<128>()) : 0;

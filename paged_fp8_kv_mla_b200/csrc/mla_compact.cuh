@@ -42,33 +42,26 @@ struct CompactParams {
   FastDiv divP, divW;              // by the page size and by row_words
 };
 
-
-// Plain loads through L2, kept on their side of the chunk's barrier.
-__device__ __forceinline__ uint4 ld_row(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_row(const uint32_t* p) {
+// A plain load through L2, kept on its side of the chunk's barrier.
+__device__ __forceinline__ uint32_t ld_word(const uint32_t* p) {
   uint32_t v;
   asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
 
-// A column of the rows of one request: element x of row t lies at base + row(t) * pitch + x, in units
-// of V, with row(t) found through a page table (table != null) or t itself (rows < limit).
-template <typename V>
+// A column of 4-byte words of the rows of one request (the scales, the accumulated weights): word x of row t lies
+// at base + row(t) * pitch + x, with row(t) found through a page table (table != null) or t itself (rows < limit).
 struct CompactColumn {
-  V* base;
+  uint32_t* base;
   long long pitch;
   const uint32_t* table;
   uint32_t pool, plane, limit;
 };
 
-// Moves the column for rows 0 .. m - 1, `per_row` elements each, U elements per thread and chunk.
-template <typename V, int THREADS, int U, typename RowOf>
+// Moves the column for rows 0 .. m - 1, `per_row` words each, U words per thread and chunk.
+template <int THREADS, int U, typename RowOf>
 __device__ __forceinline__ void compact_walk(const CompactParams& p, const int32_t* kept, uint32_t m, uint32_t per_row,
-                                             RowOf row_of, const CompactColumn<V>& col) {
+                                             RowOf row_of, const CompactColumn& col) {
   const uint32_t total = m * per_row;
   for (uint32_t e0 = 0; e0 < total; e0 += U * THREADS) {
     // three rounds of independent loads: the kept indices, the page ids, the rows
@@ -80,8 +73,8 @@ __device__ __forceinline__ void compact_walk(const CompactParams& p, const int32
       x[u] = min(e, total - 1) - to[u] * per_row;
       from[u] = e < total ? static_cast<uint32_t>(kept[to[u]]) : to[u];
     }
-    const V* src[U];
-    V* dst[U];
+    const uint32_t* src[U];
+    uint32_t* dst[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       src[u] = nullptr;
@@ -105,10 +98,10 @@ __device__ __forceinline__ void compact_walk(const CompactParams& p, const int32
       src[u] = col.base + frow * col.pitch + x[u];
       dst[u] = col.base + trow * col.pitch + x[u];
     }
-    V v[U];
+    uint32_t v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (src[u]) v[u] = ld_row(src[u]);
+      if (src[u]) v[u] = ld_word(src[u]);
     __syncthreads();                                     // the chunk has been read
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -219,15 +212,15 @@ __global__ void __launch_bounds__(THREADS, CTAS) mla_compact_kernel(const __grid
   i -= p.KVD * p.slices;
   if (i < p.KVD) {
     if (!p.scales) return;
-    const CompactColumn<uint32_t> col{reinterpret_cast<uint32_t*>(p.scales), p.row_words, slut,
-                                      static_cast<uint32_t>(p.NSB), static_cast<uint32_t>(i), ~0u};
-    compact_walk<uint32_t, THREADS, 8>(p, kept, m, p.row_words, [&](uint32_t e) { return p.divW.div(e); }, col);
+    const CompactColumn col{reinterpret_cast<uint32_t*>(p.scales), p.row_words, slut,
+                            static_cast<uint32_t>(p.NSB), static_cast<uint32_t>(i), ~0u};
+    compact_walk<THREADS, 8>(p, kept, m, p.row_words, [&](uint32_t e) { return p.divW.div(e); }, col);
     return;
   }
   if (!p.scores) return;
-  const CompactColumn<uint32_t> col{reinterpret_cast<uint32_t*>(p.scores + b * p.scores_stride), 1, nullptr, 0u, 0u,
-                                    static_cast<uint32_t>(p.scores_cols)};
-  compact_walk<uint32_t, THREADS, 8>(p, kept, m, 1, [](uint32_t e) { return e; }, col);
+  const CompactColumn col{reinterpret_cast<uint32_t*>(p.scores + b * p.scores_stride), 1, nullptr, 0u, 0u,
+                          static_cast<uint32_t>(p.scores_cols)};
+  compact_walk<THREADS, 8>(p, kept, m, 1, [](uint32_t e) { return e; }, col);
 }
 
 }  // namespace mla

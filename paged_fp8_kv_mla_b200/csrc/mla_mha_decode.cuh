@@ -52,7 +52,6 @@ constexpr int MHA_WARPS = 8;                      // consumer warps
 constexpr int MHA_THREADS = 32 * (MHA_WARPS + 4);   // consumers, and a warpgroup for the producer warp
 constexpr int MHA_ROWS = 16 * MHA_WARPS;          // rows of a CTA at most
 constexpr int MHA_MAX_STAGES = 8;
-constexpr int MHA_MAX_RUNS = 16;                  // page runs of a tile
 constexpr uint32_t MHA_SMEM_LIMIT = 232448;
 
 struct MhaParams {
