@@ -4,8 +4,12 @@
 //             + sum_{i : t <= L_b + i} sum_h exp(softmax_scale s_t <q[b,i,h,:], e4m3(code_t)> - lse[b,i,h]).
 //
 // What bounds it.  A key is 580 bytes and, at 128 heads, 2 * 128 * 576 flop: 88 ps of HBM time and
-// 88 ps of bf16 tensor time per key at a B200's measured rates, so bytes and tensor work weigh the
-// same and neither may be done twice.
+// 88 ps of bf16 tensor time per key at a B200's measured rates, so for one new token and up to 128 heads
+// bytes and tensor work weigh the same and neither is done twice.  Each further (query token, group of 128
+// heads) is an item of its own: q of one item takes 147 KB of shared memory, so a CTA walks its tiles once per
+// item and the keys come again each time, from HBM where its range is long (64 ragged requests, 2 tokens: 302 MB
+// read for 144 MB of keys).  Every item also walks to the end of its request, past the last key that its
+// token sees, so a prompt does up to twice the products that it needs.
 //
 // No conversion of the cache.  The keys go from HBM to the tensor core as the e4m3 bytes they are
 // (kind::f8f6f4) and it is q that is brought to e4m3, without loss: a bf16 value has 8 significant
@@ -36,10 +40,12 @@
 // epilogue warps take the even and the odd tiles of a request (one takes 3000 cycles a tile).
 //
 // Measured (floor): 128 requests of 8k keys, 128 heads, 149 us a call in short runs and 166 to 183 in long
-// ones (97), 16 heads 113 (94); 64 requests of 1 to 32k, 2 tokens, 79 and 88 to 94 (44); 2 short requests 7.
-// What bounds the large cases is the part's 1000 W: HBM at this rate and the 8-bit MMAs beside it bring the SM
-// clock down to 1.1 GHz (the main kernel takes 127 us at full clock), so a form on CTA pairs, with half of the
-// K reads from shared memory, took the same time and was not kept.
+// ones (97), 16 heads 113 (94), 2 tokens 297 in short runs (185); 64 requests of 1 to 32k, 2 tokens, 79 and 88 to
+// 94 (44); 2 short requests 7; a prompt of 2048 with nothing cached, 16 CTAs of work, 6.3 ms (0.18).
+// What bounds one token of many requests is the part's 1000 W: HBM at this rate and the 8-bit MMAs beside it bring
+// the SM clock down to 1.1 GHz (the main kernel takes 127 us at full clock), so a form on CTA pairs, with half of
+// the K reads from shared memory, took the same time and was not kept.  With two tokens it is the keys' second
+// pass as well: in short runs, where the cap does not act, the 8-bit pipe is at 0.55 of its rate.
 //
 // Warps: 0 K producer, 1 MMA issuer and TMEM owner, 2 q producer, 4-7 and 8-11 epilogue (each the lane
 // quadrants 0-3, for tiles of one parity).

@@ -15,10 +15,14 @@
 // What bounds it: HBM, one read and one write of every moved row.  The slices of a request are
 // neighbouring CTAs, which walk the rows at the same pace, so the 128-byte lines they share are
 // fetched once.  A request has 9 slices of 576 bytes; 128 requests of 8k cut to 4k take 120 us, 0.78 of the
-// copy rate.  With few requests the slices are 32 bytes wide (a DRAM sector) and the CTAs larger, and what
-// bounds it is the rate at which an SM's load unit takes scattered 32-byte pieces: 4 requests of 128k cut to
-// 64k 116 us, 0.4 of the copy rate on 72 SMs.  (Copies held in registers instead of shared memory: 119 and
-// 146; a cluster per slice, whose barrier waits for the writes: 134 and 141.)
+// copy rate.  With few requests the slices are 32 bytes wide (a DRAM sector) and the CTAs larger (64 registers a thread, 20 bytes spilt), and what
+// bounds it is the rate at which an SM's load unit takes scattered 32-byte pieces, on as many SMs as there are
+// slices: 4 requests of 128k cut to 64k 113 us, 0.4 of the copy rate on 72 SMs, and one such request 110 (floor
+// 12) on 18.  (Copies held in registers instead of shared memory: 119 and 146; a cluster per slice, whose barrier
+// waits for the writes: 134 and 141.)  The words of a column (scales, sums) are walked by one CTA, a chunk at a time:
+// for one scale a token that ends with the rows, but the scales of an e4m3 cache with 8 kv heads of 128 are what a
+// long request waits for: 4 of 128k to 64k 854 us (floor 169; bf16, without scales, 457 of 328), 32 of 8k to 4k 133
+// (85; bf16 192 of 164).
 #pragma once
 #include <cstdint>
 #include "mla_kernels.cuh"

@@ -24,7 +24,7 @@
 //
 // e4m3.  The values are converted to f16, exactly, as they leave shared memory (two per instruction),
 // and never to anything wider: each row of q is brought to f16 with a power of two of its own (exact down to
-// 2^-30 of the row's largest value, and no row depends on those beside it), K's scale multiplies the score, and V's scale goes into the weight, relative to a
+// 2^-30 of the row's largest value, whatever the rows beside it hold), K's scale multiplies the score, and V's scale goes into the weight, relative to a
 // running power-of-two bound of V's scales so that f16 holds it with 11 bits (down to 2^-23 of the bound).
 // The instructions of this are what keeps an e4m3 cache from the copy rate: the loads alone run at it.  (One power
 // of two for a warp's rows together cost nothing elsewhere, but took 130 instead of 140 us for 64 requests of 8k, 16
@@ -39,9 +39,13 @@
 // left out.
 //
 // Measured (floor, the cache's bytes at the copy rate): 64 requests of 1 to 32k, 2 tokens, 32/8 heads of 128,
-// bf16 165 us (155), e4m3 97 (80); 128 of 8k, 64/8 heads of 128, e4m3 334 to 376 by machine (338); heads of 64,
-// e4m3 193 (174); 2 short requests 5.6.  Above 8 rows a head (16 here: 224, floor 170) and with one kv head (66,
-// floor 42) the latency of a warp's own chain shows, with two warps to a scheduler.
+// bf16 165 us (155), e4m3 97 (80); 128 of 8k, 64/8 heads of 128, e4m3 337 to 376 by machine (338); heads of 64,
+// e4m3 200 (174); 2 short requests 5.6.  Above 8 rows a head (64 of 8k, 128/8 heads: 226, floor 170) and with one kv
+// head (128 of 8k: 69, floor 42) the latency of a warp's own chain shows, with two warps to a scheduler.  All
+// eight variants with heads of 128 and five of the ten with heads of 64 spill 24 to 88 bytes at the launch's 168
+// registers a thread.  Prompts are right but far from what a prefill takes: every row group
+// walks to its request's end, past the last key its rows see, and reads K and V again (2048 tokens, nothing cached, 32/8
+// heads of 128, bf16: 328 us, floor 21).
 #pragma once
 #include <cstdint>
 #include "mla_kernels.cuh"

@@ -1,4 +1,4 @@
-"""Multi-head decode: a query row's result depends on that row alone, whatever the rows beside it hold.
+"""Multi-head decode: a query row's result is right whatever the rows beside it hold.
 
 The rows that share a kv head (tokens of a step and heads of a group) are computed side by side in one
 warp.  Tolerances are those of test_gpu_mha.check, whose terms are the row's own."""
